@@ -84,7 +84,13 @@ typedef enum {
 #define GG_DEV_TIMEOUT      0x4u  /* a pipeline wait exceeded the watchdog; results of this
                                      call are incomplete                                  */
 #define GG_DEV_BAD_ROUTE    0x8u  /* gg_route: an expert id was >= E; that assignment was
-                                     dropped                                              */
+                                     dropped. gg_unroute, gg_silu_mul and their gradients: a
+                                     row_of entry was past the rows (in use); it was dropped.
+                                     gg_gate_topk_backward: an id was >= E; it was dropped   */
+#define GG_DEV_BAD_LOGIT    0x10u /* gg_gate_topk: a logit of a token in use was NaN or +inf, or
+                                     its bias was; that expert was treated as masked       */
+#define GG_DEV_BAD_COUNT    0x20u /* *rows_used or *num_tokens was negative or above the
+                                     allocated rows or tokens; it was clamped               */
 #define GG_DEV_ERROR_MASK   0xFFu
 #define GG_DEV_LAUNCHED     0x100u /* informational: the sm_100a kernel ran to its end     */
 
@@ -258,6 +264,127 @@ GG_API gg_status gg_route(const int32_t* topk_ids, int64_t T_tok, int32_t k, int
 GG_API gg_status gg_route_noalloc(const int32_t* topk_ids, int64_t T_tok, int32_t k, int32_t E,
                                   const void* X, int64_t K, void* A_packed, int32_t* row_of,
                                   int32_t* offs, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The gate: each token's k experts and their weights from the router's logits (the step
+ * before gg_route; the pages take top-k ids as given).
+ *   logits     bf16 [T, E], or fp32 with GG_GATE_LOGITS_F32
+ *   bias       fp32 [E] or NULL, GG_GATE_SIGMOID only: added to the score for the choice, not
+ *              for the weight (a balancing bias)
+ *   score      GG_GATE_SOFTMAX: p = softmax(x) over the token's experts;
+ *              GG_GATE_SIGMOID: p = 1 / (1 + e^-x)
+ *   flags      GG_GATE_RENORM: the weights are scale * p / (sum of the k chosen p), else
+ *              scale * p; the sum is taken relative to the largest of the chosen, so it
+ *              neither underflows nor overflows
+ *   num_tokens int32, device, or NULL (T): tokens in use of a padded batch; the logits of the
+ *              others are not read, their ids are -1 and their weights 0
+ *   topk_ids   int32 [T, k], best first, ties to the lowest expert (-0 equals +0); weights
+ *              fp32 [T, k]
+ * Without a bias the choice goes by the logits themselves (exact), with one by the scores in
+ * double precision. An expert with logit (or bias) -inf is masked: it is never chosen and has
+ * no probability. A token with fewer than k unmasked experts gets ids -1 and weights 0 in its
+ * last slots; gg_route drops those. NaN and +inf count as masked and set GG_DEV_BAD_LOGIT.
+ * A mask of the type's lowest finite value is an ordinary, very small logit.
+ * k <= E, k <= GG_GATE_MAX_K, E <= GG_MAX_EXPERTS; logits need the alignment of their type.
+ */
+#define GG_GATE_SOFTMAX 0
+#define GG_GATE_SIGMOID 1
+#define GG_GATE_RENORM 0x1
+#define GG_GATE_LOGITS_F32 0x2
+#define GG_GATE_MAX_K 32
+GG_API gg_status gg_gate_topk(const void* logits, int64_t T, int32_t E, int32_t k,
+                              const float* bias, int32_t score, int32_t flags, float scale,
+                              const int32_t* num_tokens, int32_t* topk_ids, float* weights,
+                              int32_t* dev_status, cudaStream_t stream);
+
+/* Gradient of the logits of gg_gate_topk from dweights fp32 [T, k]; score, flags and scale as
+   in the forward call, topk_ids its result (slots of id -1 carry nothing). dlogits, in the
+   logits' type, is written in full: 0 for every logit that the weights do not depend on, and
+   for tokens without an id. Not in place (dlogits must not overlap logits). */
+GG_API gg_status gg_gate_topk_backward(const void* logits, int64_t T, int32_t E, int32_t k,
+                                       int32_t score, int32_t flags, float scale,
+                                       const int32_t* topk_ids, const float* dweights,
+                                       void* dlogits, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The way back from the packed layout (the step after the path; without weights and residual
+ * it is the gradient of gg_route's A_packed with respect to X):
+ *   out[t, :] = residual[t, :] + sum over s of weights[t, s] * Y[row_of[t*k + s], :]
+ *   Y bf16 [rows, N]; row_of int32 [T_tok*k] as gg_route writes it (-1: dropped, adds
+ *   nothing); weights fp32 [T_tok, k] or NULL (1); residual bf16 [T_tok, N] or NULL (0), may
+ *   be out itself; out bf16 [T_tok, N], every row written.
+ * fp32 sums in the order of the slots, rounded once; the result does not depend on the launch.
+ * Rows that no entry names are not read; the weight of a dropped slot is not read.
+ */
+GG_API gg_status gg_unroute(const void* Y, int64_t rows, const int32_t* row_of,
+                            const float* weights, const void* residual, int64_t T_tok, int32_t k,
+                            int64_t N, void* out, int32_t* dev_status, cudaStream_t stream);
+
+/* Gradients of gg_unroute: dY[row_of[i], :] = weights[i] * dout[t, :] and dweights[i] =
+   <dout[t, :], Y[row_of[i], :]> for assignment i = t*k + s (0 when dropped). dY bf16 [rows, N]
+   or NULL; dweights fp32 [T_tok, k] or NULL (Y is read only for it). row_of's rows must be
+   distinct, as gg_route makes them, and lie below *rows_used where that is given; rows of dY
+   that no entry names are left as they are, but with GG_FLAG_ZERO_TAIL the rows at and past
+   *rows_used (int32, device; e.g. &offs[E-1]) become +0.0. */
+GG_API gg_status gg_unroute_backward(const void* dout, const void* Y, int64_t rows,
+                                     const int32_t* row_of, const float* weights, int64_t T_tok,
+                                     int32_t k, int64_t N, const int32_t* rows_used,
+                                     int32_t flags, void* dY, float* dweights,
+                                     int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * SiLU-and-mul between the two expert products, for training: gg_forward_ex's fused form
+ * keeps nothing for the backward pass, this one takes the first product's output H and can
+ * keep it in 8 bits (see gg_pack8), so that H itself need not live until the backward pass.
+ *   act[r, j] = weight * silu(g_j) * u_j,  j < I = N / 2, g and u the gate and up columns of
+ *   H[r, :] (bf16 [rows, N]): interleaved in blocks of 128 (N % 256 == 0) or, with
+ *   GG_FLAG_GATE_UP_CONCAT, the halves [gate | up] (N % 16 == 0), as in gg_forward_ex.
+ * Rows: r < *rows_used (int32, device, e.g. &offs[E-1]; NULL: all rows), weight = weights[r];
+ * or, with row_of int32 [n_assign], r = row_of[i] and weight = weights[i] for assignment i (the
+ * routing weights in the order of gg_gate_topk; entries distinct or -1, below *rows_used where
+ * that is given). weights NULL: 1. Other rows are neither read nor written, but with
+ * GG_FLAG_ZERO_TAIL the rows of act at and past *rows_used become +0.0.
+ *   act bf16 [rows, I]; H8 e4m3 [rows, N] in the columns' order of H and H8_scale uint8
+ *   [rows, 2 * ceil(I / 32)] (both or neither NULL): the 8-bit form of gg_pack8, with blocks of
+ *   32 gate columns and of 32 up columns; their codes lie in the columns' order of H.
+ */
+GG_API gg_status gg_silu_mul(const void* H, int64_t rows, int64_t N, const int32_t* rows_used,
+                             const int32_t* row_of, int64_t n_assign, const float* weights,
+                             int32_t flags, void* act, void* H8, void* H8_scale,
+                             int32_t* dev_status, cudaStream_t stream);
+
+/* Gradients of gg_silu_mul, from H8 and H8_scale (H NULL) or from H (those NULL):
+     dg = weight * dact * u * q (1 + g (1 - q)),  du = weight * dact * g * q,  q = 1 / (1 + e^-g)
+   into dH bf16 [rows, N]; act (bf16 [rows, I], may be NULL) is computed again from the same
+   values, as the second product's wgrad needs it; dweights fp32, indexed like weights (may be
+   NULL): <dact, silu(g) * u> of the row, 0 for a dropped assignment (without row_of, entries
+   of rows that are not in use are left as they are). GG_FLAG_ZERO_TAIL clears the tail of dH
+   and act. */
+GG_API gg_status gg_silu_mul_backward(const void* dact, const void* H, const void* H8,
+                                      const void* H8_scale, int64_t rows, int64_t N,
+                                      const int32_t* rows_used, const int32_t* row_of,
+                                      int64_t n_assign, const float* weights, int32_t flags,
+                                      void* dH, void* act, float* dweights, int32_t* dev_status,
+                                      cudaStream_t stream);
+
+/*
+ * The 8-bit row form: X8[r, c] = e4m3(X[r, c] / s), rounded to nearest even, with one scale s =
+ * 2^(code - 127) for 32 columns (the last block of a row may be shorter), code the least in
+ * [9, 247] with max |X| <= 448 s. The division is exact, so a value is off by at most 2^-4 of
+ * itself, or by 2^-10 s below 2^-6 s. (Under code 247 magnitudes above 240 s become 240 s: the
+ * next value is past bf16's range.) NaN stays NaN, and an infinity becomes NaN (neither counts
+ * for the scale).
+ *   X bf16 [rows, cols], cols % 8 == 0; X8 e4m3 [rows, cols]; scale uint8 [rows,
+ *   ceil(cols / 32)], the codes; rows at and past *rows_used (NULL: none) are not touched.
+ */
+GG_API gg_status gg_pack8(const void* X, int64_t rows, int64_t cols, const int32_t* rows_used,
+                          void* X8, void* scale, int32_t* dev_status, cudaStream_t stream);
+
+/* X[r, c] = X8[r, c] * 2^(code - 127), exact in bf16 for what gg_pack8 wrote. Rows at and past
+   *rows_used are left as they are, or become +0.0 with GG_FLAG_ZERO_TAIL. */
+GG_API gg_status gg_unpack8(const void* X8, const void* scale, int64_t rows, int64_t cols,
+                            const int32_t* rows_used, int32_t flags, void* X,
+                            int32_t* dev_status, cudaStream_t stream);
 
 /* A static, human-readable name for a status. */
 /*

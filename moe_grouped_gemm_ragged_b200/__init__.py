@@ -26,6 +26,8 @@ DEV_BAD_OFFSETS = 0x1
 DEV_BAD_MASKED_M = 0x2
 DEV_TIMEOUT = 0x4
 DEV_BAD_ROUTE = 0x8
+DEV_BAD_LOGIT = 0x10
+DEV_BAD_COUNT = 0x20
 DEV_ERROR_MASK = 0xFF
 DEV_LAUNCHED = 0x100
 MAX_EXPERTS = 1024
@@ -95,6 +97,7 @@ def lib() -> ctypes.CDLL:
     L.gg_testing_force_variant.argtypes = [ctypes.c_int]
     L.gg_testing_force_variant.restype = ctypes.c_int
     L.gg_version.restype = ctypes.c_int
+    _layer.declare(L)
     L.gg_last_error.restype = ctypes.c_char_p
     _lib = L
     return L
@@ -476,43 +479,59 @@ class _GroupedMM(torch.autograd.Function):
     groups. Output and input gradient are complete tensors (zero past the last offset)."""
 
     @staticmethod
-    def forward(ctx, A, W, offs, w_nk):
+    def forward(ctx, A, W, offs, w_nk, ckpt8):
         N = W.shape[1] if w_nk else W.shape[2]
         out = torch.empty((A.shape[0], N), dtype=A.dtype, device=A.device)
         forward_ex(A, W, offs, out, zero_tail=True, w_nk=w_nk)
-        ctx.save_for_backward(A, W, offs)
         ctx.w_nk = w_nk
+        A8 = scale = None
+        if ckpt8:  # A is only needed for the wgrad
+            if ctx.needs_input_grad[1]:
+                A8, scale = _layer.pack8(A, offs=offs)
+            A = None
+        ctx.save_for_backward(A, W, offs, A8, scale)
         return out
 
     @staticmethod
     def backward(ctx, dout):
-        A, W, offs = ctx.saved_tensors
+        A, W, offs, A8, scale = ctx.saved_tensors
         dout = dout.contiguous()
         dA = dW = None
         if ctx.needs_input_grad[0]:
-            dA = torch.empty_like(A)
+            K = W.shape[2] if ctx.w_nk else W.shape[1]
+            dA = torch.empty((dout.shape[0], K), dtype=dout.dtype, device=dout.device)
             dgrad_ex(dout, W, offs, dA, zero_tail=True, w_nk=ctx.w_nk)
         if ctx.needs_input_grad[1]:
+            if A8 is not None:
+                A = _layer.unpack8(A8, scale, offs=offs)
             dW = torch.empty_like(W)
             wgrad_ex(A, dout, offs, dW, w_nk=ctx.w_nk)
-        return dA, dW, None, None
+        return dA, dW, None, None, None
 
 
 def grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torch.Tensor,
-               out: Optional[torch.Tensor] = None, *, w_nk: bool = False) -> torch.Tensor:
+               out: Optional[torch.Tensor] = None, *, w_nk: bool = False,
+               ckpt8: bool = False) -> torch.Tensor:
     """``torch._grouped_mm(x, w, offs)``-style call (PyTorch issue 152668). With autograd
     (A or W requiring grad) the backward runs gg_dgrad / gg_wgrad and rows past the last
     offset are zero in the output and in dA. Without autograd, ``out`` may be given (rows
-    past the last offset are then left as they are)."""
+    past the last offset are then left as they are). With ``ckpt8`` A is kept for the wgrad in
+    8 bits (``pack8``), about half its bytes, and dW is the product with these values."""
     if torch.is_grad_enabled() and (A.requires_grad or W.requires_grad):
         if out is not None:
             raise ValueError("out= cannot be used with autograd")
-        return _GroupedMM.apply(A, W, offs, w_nk)
+        return _GroupedMM.apply(A, W, offs, w_nk, ckpt8)
     if out is None:
         N = W.shape[1] if w_nk else W.shape[2]
         out = torch.empty((A.shape[0], N), dtype=A.dtype, device=A.device)
     return forward_ex(A, W, offs, out, w_nk=w_nk)
 
+
+from . import _layer  # noqa: E402  (it builds on the functions above)
+from ._layer import (  # noqa: E402
+    GATE_MAX_K, GATE_SIGMOID, GATE_SOFTMAX, combine, dispatch, expert_mlp, gate, gate_topk,
+    gate_topk_backward, pack8, silu_mul, silu_mul_backward, swiglu, unpack8, unroute,
+    unroute_backward)
 
 __all__ = [
     "forward", "forward_ex", "dgrad", "dgrad_ex", "wgrad", "wgrad_ex", "wgrad_f32",
@@ -521,6 +540,10 @@ __all__ = [
     "grouped_mm", "layer_step_host", "status_string", "version",
     "set_watchdog_ns", "testing_skip_first_load", "testing_force_variant", "lib", "GGError",
     "LIB_PATH",
+    "gate", "gate_topk", "gate_topk_backward", "GATE_SOFTMAX", "GATE_SIGMOID", "GATE_MAX_K",
+    "dispatch", "combine", "unroute", "unroute_backward", "expert_mlp", "swiglu", "silu_mul",
+    "silu_mul_backward", "pack8", "unpack8",
+    "DEV_BAD_ROUTE", "DEV_BAD_LOGIT", "DEV_BAD_COUNT",
     "DEV_BAD_OFFSETS", "DEV_BAD_MASKED_M", "DEV_TIMEOUT", "DEV_ERROR_MASK", "DEV_LAUNCHED",
     "MAX_EXPERTS",
 ]

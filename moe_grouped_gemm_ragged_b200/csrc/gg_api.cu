@@ -15,6 +15,7 @@
 #include "gg.h"
 #include "gg_kernel.cuh"
 #include "gg_masked.cuh"
+#include "gg_ops.cuh"
 
 namespace {
 
@@ -740,6 +741,22 @@ gg_status masked_impl(const void* A, const void* W, const int32_t* masked_m, voi
 }
 
 }  // namespace
+
+namespace gg {
+namespace ops {
+
+gg_status device_sms(int* sms) {
+  DeviceInfo di;
+  const gg_status s = device_info(&di);
+  if (s != GG_OK) return s;
+  *sms = di.sms;
+  return di.sm100 ? GG_OK : GG_ERR_UNSUPPORTED;
+}
+
+gg_status cuda_failed(const char* where, cudaError_t e) { return cuda_fail(where, e); }
+
+}  // namespace ops
+}  // namespace gg
 
 extern "C" {
 
