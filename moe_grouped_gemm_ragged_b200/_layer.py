@@ -10,15 +10,14 @@ support being differentiated again.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (FLAG_GATE_UP_CONCAT, FLAG_ZERO_TAIL, _check, _ptr, _raise, _status_ptr,
-               _stream_handle, dgrad_ex, forward_ex, lib, route, wgrad_ex)
+from . import (FLAG_GATE_UP_CONCAT, FLAG_ZERO_TAIL, _check, _raise, _status_ptr, _stream_handle,
+               dgrad_ex, forward_ex, lib, route, wgrad_ex)
 
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 GATE_RENORM, GATE_LOGITS_F32 = 0x1, 0x2
@@ -48,30 +47,32 @@ def declare(L: ctypes.CDLL) -> None:
 
 def _on(stream):
     """Allocate for the stream that the call runs on, not for the current one."""
-    if stream is None:
-        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 
-def _buffer(t, name, shape, dtype, device, stream):
-    """The caller's buffer, checked, or a new one."""
+def _arg(t, name, shape, dtype, dev) -> Optional[int]:
+    """Address of an argument of this shape and type (None: NULL) on device ``dev``, the current
+    one. One combined test for the usual case, the messages of ``_check`` for the others."""
     if t is None:
-        with _on(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
-
-
-def _optional(t, name, shape, dtype):
-    if t is not None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.get_device() == dev and t.is_contiguous()):
         _check(t, name, dtype, len(shape))
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t)
+    return t.data_ptr()
+
+
+def _new(t, shape, dtype, like, stream):
+    """The caller's buffer, or a new one."""
+    if t is not None:
+        return t
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _used_ptr(offs, zero_tail):
@@ -95,7 +96,8 @@ def _gate_args(logits, k, score, renorm, scale):
     if score not in (GATE_SOFTMAX, GATE_SIGMOID):
         raise ValueError("score must be GATE_SOFTMAX or GATE_SIGMOID")
     flags = (GATE_RENORM if renorm else 0) | (GATE_LOGITS_F32 if logits.dtype is _F32 else 0)
-    return logits.shape[0], logits.shape[1], int(k), int(score), flags, float(scale)
+    T, E = logits.shape
+    return T, E, int(k), int(score), flags, float(scale), logits.get_device()
 
 
 def gate_topk(logits: torch.Tensor, k: int, *, score: int = GATE_SOFTMAX, renorm: bool = True,
@@ -111,14 +113,15 @@ def gate_topk(logits: torch.Tensor, k: int, *, score: int = GATE_SOFTMAX, renorm
     (GATE_SIGMOID only) is added to the scores for the choice alone. Logits of -inf are masked;
     a token with fewer than k others gets ids -1, which ``route`` drops, and weights 0 in its
     last slots. ``num_tokens`` int32 [1]: tokens in use of a padded batch, read on the device."""
-    T, E, k, score, flags, scale = _gate_args(logits, k, score, renorm, scale)
+    T, E, k, score, flags, scale, dev = _gate_args(logits, k, score, renorm, scale)
     if k < 1:
         raise ValueError("k must be positive")
-    ids = _buffer(topk_ids, "topk_ids", (T, k), _I32, logits.device, stream)
-    w = _buffer(weights, "weights", (T, k), _F32, logits.device, stream)
-    rc = lib().gg_gate_topk(_ptr(logits), T, E, k, _optional(bias, "bias", (E,), _F32), score,
-                            flags, scale, _optional(num_tokens, "num_tokens", (1,), _I32),
-                            _ptr(ids), _ptr(w), _status_ptr(status), _stream_handle(stream))
+    ids = _new(topk_ids, (T, k), _I32, logits, stream)
+    w = _new(weights, (T, k), _F32, logits, stream)
+    rc = lib().gg_gate_topk(
+        logits.data_ptr(), T, E, k, _arg(bias, "bias", (E,), _F32, dev), score, flags, scale,
+        _arg(num_tokens, "num_tokens", (1,), _I32, dev), _arg(ids, "topk_ids", (T, k), _I32, dev),
+        _arg(w, "weights", (T, k), _F32, dev), _status_ptr(status), _stream_handle(stream))
     _raise(rc, "gg_gate_topk")
     return ids, w
 
@@ -130,13 +133,15 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
     """Gradient of the logits (in their type, written in full) from that of the weights;
     ``topk_ids`` is what ``gate_topk`` returned for the same score, renorm and scale."""
     _check(topk_ids, "topk_ids", _I32, 2)
-    T, E, k, score, flags, scale = _gate_args(logits, topk_ids.shape[1], score, renorm, scale)
+    T, E, k, score, flags, scale, dev = _gate_args(logits, topk_ids.shape[1], score, renorm,
+                                                   scale)
     if topk_ids.shape[0] != T:
         raise ValueError("topk_ids[T, k] and logits[T, E] disagree on T")
-    out = _buffer(dlogits, "dlogits", (T, E), logits.dtype, logits.device, stream)
+    out = _new(dlogits, (T, E), logits.dtype, logits, stream)
     rc = lib().gg_gate_topk_backward(
-        _ptr(logits), T, E, k, score, flags, scale, _ptr(topk_ids),
-        _optional(dweights, "dweights", (T, k), _F32), _ptr(out), _status_ptr(status),
+        logits.data_ptr(), T, E, k, score, flags, scale, topk_ids.data_ptr(),
+        _arg(dweights, "dweights", (T, k), _F32, dev),
+        _arg(out, "dlogits", (T, E), logits.dtype, dev), _status_ptr(status),
         _stream_handle(stream))
     _raise(rc, "gg_gate_topk_backward")
     return out
@@ -145,11 +150,12 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
 # ---------------------------------------------------------------------------------- unroute
 
 def _tokens(row_of, k):
+    """(tokens, k, address) of row_of."""
     _check(row_of, "row_of", _I32, 1)
-    k = int(k)
-    if k < 1 or row_of.numel() % k != 0:
+    k, n = int(k), row_of.numel()
+    if k < 1 or n % k != 0:
         raise ValueError("row_of must hold k entries for each token")
-    return row_of.numel() // k, k
+    return n // k, k, row_of.data_ptr()
 
 
 def unroute(Y: torch.Tensor, row_of: torch.Tensor, k: int, out: Optional[torch.Tensor] = None, *,
@@ -161,13 +167,14 @@ def unroute(Y: torch.Tensor, row_of: torch.Tensor, k: int, out: Optional[torch.T
     Y bf16 [rows, N]; row_of int32 [T*k] from ``route`` (-1 adds nothing); weights float32 [T, k]
     (None: 1); residual bf16 [T, N] (None: 0; may be ``out``); out bf16 [T, N]."""
     _check(Y, "Y", _BF16, 2)
-    T, k = _tokens(row_of, k)
+    T, k, rp = _tokens(row_of, k)
     rows, N = Y.shape
-    out = _buffer(out, "out", (T, N), _BF16, Y.device, stream)
-    rc = lib().gg_unroute(_ptr(Y), rows, _ptr(row_of),
-                          _optional(weights, "weights", (T, k), _F32),
-                          _optional(residual, "residual", (T, N), _BF16), T, k, N, _ptr(out),
-                          _status_ptr(status), _stream_handle(stream))
+    dev = Y.get_device()
+    out = _new(out, (T, N), _BF16, Y, stream)
+    rc = lib().gg_unroute(Y.data_ptr(), rows, rp, _arg(weights, "weights", (T, k), _F32, dev),
+                          _arg(residual, "residual", (T, N), _BF16, dev), T, k, N,
+                          _arg(out, "out", (T, N), _BF16, dev), _status_ptr(status),
+                          _stream_handle(stream))
     _raise(rc, "gg_unroute")
     return out
 
@@ -184,7 +191,7 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
     those past the last of ``offs`` become zeros. row_of's rows must be distinct. Returns
     (dY, dweights)."""
     _check(dout, "dout", _BF16, 2)
-    T, k = _tokens(row_of, k)
+    T, k, rp = _tokens(row_of, k)
     N = dout.shape[1]
     if dout.shape[0] != T:
         raise ValueError("dout must have a row for each token")
@@ -193,11 +200,12 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
     if dweights is not None and Y is None:
         raise ValueError("dweights needs Y")
     rows = (dY if dY is not None else Y).shape[0]
+    dev = dout.get_device()
     rc = lib().gg_unroute_backward(
-        _ptr(dout), _optional(Y, "Y", (rows, N), _BF16), rows, _ptr(row_of),
-        _optional(weights, "weights", (T, k), _F32), T, k, N, _used_ptr(offs, zero_tail),
-        FLAG_ZERO_TAIL if zero_tail else 0, _optional(dY, "dY", (rows, N), _BF16),
-        _optional(dweights, "dweights", (T, k), _F32), _status_ptr(status),
+        dout.data_ptr(), _arg(Y, "Y", (rows, N), _BF16, dev), rows, rp,
+        _arg(weights, "weights", (T, k), _F32, dev), T, k, N, _used_ptr(offs, zero_tail),
+        FLAG_ZERO_TAIL if zero_tail else 0, _arg(dY, "dY", (rows, N), _BF16, dev),
+        _arg(dweights, "dweights", (T, k), _F32, dev), _status_ptr(status),
         _stream_handle(stream))
     _raise(rc, "gg_unroute_backward")
     return dY, dweights
@@ -212,11 +220,12 @@ def _half_blocks(N):
 def _act_args(rows, offs, row_of, weights, gate_up_concat, zero_tail):
     """(rows_used, row_of, n_assign, weights, flags): pointers and sizes of the C call."""
     used = _used_ptr(offs, zero_tail)
-    n = rows
+    n, rp, na = rows, None, 0
     if row_of is not None:
         _check(row_of, "row_of", _I32, 1)
-        n = row_of.numel()
-    return (used, _ptr(row_of), 0 if row_of is None else n, _per_row(weights, "weights", n),
+        n = na = row_of.numel()
+        rp = row_of.data_ptr()
+    return (used, rp, na, _per_row(weights, "weights", n),
             (FLAG_ZERO_TAIL if zero_tail else 0) | (FLAG_GATE_UP_CONCAT if gate_up_concat else 0))
 
 
@@ -232,11 +241,12 @@ def _per_row(t, name, n):
     return t.data_ptr()
 
 
-def _check8(x8, scale, what, rows, cols, codes):
+def _args8(x8, scale, rows, cols, codes, dev):
+    """Addresses of the 8-bit rows and their scales."""
     if (x8 is None) != (scale is None):
-        raise ValueError(f"{what} and {what}_scale go together")
-    return (_optional(x8, what, (rows, cols), _E4M3),
-            _optional(scale, f"{what}_scale", (rows, codes), _E8M0))
+        raise ValueError("H8 and H8_scale go together")
+    return (_arg(x8, "H8", (rows, cols), _E4M3, dev),
+            _arg(scale, "H8_scale", (rows, codes), _E8M0, dev))
 
 
 def silu_mul(H: torch.Tensor, act: Optional[torch.Tensor] = None, *,
@@ -255,10 +265,12 @@ def silu_mul(H: torch.Tensor, act: Optional[torch.Tensor] = None, *,
     of H are also kept there in 8 bits, for ``silu_mul_backward``."""
     _check(H, "H", _BF16, 2)
     rows, N = H.shape
+    dev = H.get_device()
     used, rp, n, wp, flags = _act_args(rows, offs, row_of, weights, gate_up_concat, zero_tail)
-    p8, ps = _check8(H8, H8_scale, "H8", rows, N, _half_blocks(N))
-    act = _buffer(act, "act", (rows, N // 2), _BF16, H.device, stream)
-    rc = lib().gg_silu_mul(_ptr(H), rows, N, used, rp, n, wp, flags, _ptr(act), p8, ps,
+    p8, ps = _args8(H8, H8_scale, rows, N, _half_blocks(N), dev)
+    act = _new(act, (rows, N // 2), _BF16, H, stream)
+    rc = lib().gg_silu_mul(H.data_ptr(), rows, N, used, rp, n, wp, flags,
+                           _arg(act, "act", (rows, N // 2), _BF16, dev), p8, ps,
                            _status_ptr(status), _stream_handle(stream))
     _raise(rc, "gg_silu_mul")
     return act
@@ -279,15 +291,17 @@ def silu_mul_backward(dact: torch.Tensor, dH: Optional[torch.Tensor] = None, *,
     weights' gradient into ``dweights`` (float32, indexed like the weights; 0 for a dropped
     assignment)."""
     _check(dact, "dact", _BF16, 2)
-    rows, N = dact.shape[0], 2 * dact.shape[1]
+    rows, half = dact.shape
+    N, dev = 2 * half, dact.get_device()
     if (H is None) == (H8 is None):
         raise ValueError("exactly one of H and H8 must be given")
     used, rp, n, wp, flags = _act_args(rows, offs, row_of, weights, gate_up_concat, zero_tail)
-    p8, ps = _check8(H8, H8_scale, "H8", rows, N, _half_blocks(N))
-    dH = _buffer(dH, "dH", (rows, N), _BF16, dact.device, stream)
+    p8, ps = _args8(H8, H8_scale, rows, N, _half_blocks(N), dev)
+    dH = _new(dH, (rows, N), _BF16, dact, stream)
     rc = lib().gg_silu_mul_backward(
-        _ptr(dact), _optional(H, "H", (rows, N), _BF16), p8, ps, rows, N, used, rp, n, wp, flags,
-        _ptr(dH), _optional(act, "act", (rows, N // 2), _BF16),
+        dact.data_ptr(), _arg(H, "H", (rows, N), _BF16, dev), p8, ps, rows, N, used, rp, n, wp,
+        flags, _arg(dH, "dH", (rows, N), _BF16, dev),
+        _arg(act, "act", (rows, half), _BF16, dev),
         _per_row(dweights, "dweights", rows if row_of is None else n), _status_ptr(status),
         _stream_handle(stream))
     _raise(rc, "gg_silu_mul_backward")
@@ -302,11 +316,13 @@ def pack8(X: torch.Tensor, X8: Optional[torch.Tensor] = None,
     Rows at and past the last of ``offs`` are not touched."""
     _check(X, "X", _BF16, 2)
     rows, cols = X.shape
-    X8 = _buffer(X8, "X8", (rows, cols), _E4M3, X.device, stream)
-    scale = _buffer(scale, "scale", (rows, (cols + BLOCK8 - 1) // BLOCK8), _E8M0, X.device,
-                    stream)
-    rc = lib().gg_pack8(_ptr(X), rows, cols, _used_ptr(offs, False), _ptr(X8), _ptr(scale),
-                        _status_ptr(status), _stream_handle(stream))
+    codes, dev = (cols + BLOCK8 - 1) // BLOCK8, X.get_device()
+    X8 = _new(X8, (rows, cols), _E4M3, X, stream)
+    scale = _new(scale, (rows, codes), _E8M0, X, stream)
+    rc = lib().gg_pack8(X.data_ptr(), rows, cols, _used_ptr(offs, False),
+                        _arg(X8, "X8", (rows, cols), _E4M3, dev),
+                        _arg(scale, "scale", (rows, codes), _E8M0, dev), _status_ptr(status),
+                        _stream_handle(stream))
     _raise(rc, "gg_pack8")
     return X8, scale
 
@@ -317,12 +333,12 @@ def unpack8(X8: torch.Tensor, scale: torch.Tensor, X: Optional[torch.Tensor] = N
     """X bf16 [rows, cols] = X8 * scale, exact for what ``pack8`` wrote."""
     _check(X8, "X8", _E4M3, 2)
     rows, cols = X8.shape
-    X = _buffer(X, "X", (rows, cols), _BF16, X8.device, stream)
-    rc = lib().gg_unpack8(_ptr(X8),
-                          _optional(scale, "scale", (rows, (cols + BLOCK8 - 1) // BLOCK8), _E8M0),
-                          rows, cols, _used_ptr(offs, zero_tail),
-                          FLAG_ZERO_TAIL if zero_tail else 0, _ptr(X), _status_ptr(status),
-                          _stream_handle(stream))
+    dev = X8.get_device()
+    X = _new(X, (rows, cols), _BF16, X8, stream)
+    rc = lib().gg_unpack8(
+        X8.data_ptr(), _arg(scale, "scale", (rows, (cols + BLOCK8 - 1) // BLOCK8), _E8M0, dev),
+        rows, cols, _used_ptr(offs, zero_tail), FLAG_ZERO_TAIL if zero_tail else 0,
+        _arg(X, "X", (rows, cols), _BF16, dev), _status_ptr(status), _stream_handle(stream))
     _raise(rc, "gg_unpack8")
     return X
 
