@@ -1,8 +1,10 @@
 // The gate before the routing: each token's k experts and their weights from the router's
-// logits, and the gradient of the logits from the gradient of the weights. One warp takes a
-// token; its logits stay in registers.
+// logits, and the gradient of the logits from the gradient of the weights. A group of 4 to 32
+// lanes takes a token, each lane 8 or more neighbouring experts: their logits are one or two
+// wide loads and stay in registers. What bounds these kernels is instructions, not bytes.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "gg_ops.cuh"
 
@@ -12,7 +14,6 @@ namespace gate {
 using namespace gg::ops;
 
 constexpr int THREADS = 128;
-constexpr int WARPS = THREADS / 32;
 constexpr uint32_t ALL = 0xffffffffu;
 
 struct Params {
@@ -30,19 +31,104 @@ struct Params {
   float scale;
 };
 
-__device__ __forceinline__ float load(const float* p) { return *p; }
-__device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// NV neighbouring logits of a row (first: the lane's first expert); the rest of the lane's
+// share, past E, is masked. wide: E is a multiple of 8 and the rows start on 16 bytes.
+template <int NV>
+__device__ __forceinline__ void load_row(const float* row, int first, int E, bool wide,
+                                         float (&x)[NV]) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(ALL, v, d);
+  for (int j = 0; j < NV; j += 4) {
+    if (NV >= 4 && wide && first + j < E) {
+      const float4 v = *reinterpret_cast<const float4*>(row + first + j);
+      x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 4 && i < NV; ++i) x[i] = first + i < E ? row[first + i] : -INFINITY;
+    }
+  }
+}
+template <int NV>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* row, int first, int E, bool wide,
+                                         float (&x)[NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; j += 8) {
+    if (NV >= 8 && wide && first + j < E) {
+      float v[8];
+      unpack_bf16(*reinterpret_cast<const uint4*>(row + first + j), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j + i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 8 && i < NV; ++i)
+        x[i] = first + i < E ? __bfloat162float(row[first + i]) : -INFINITY;
+    }
+  }
+}
+template <int NV>
+__device__ __forceinline__ void store_row(float* row, int first, int E, bool wide,
+                                          const float* x) {
+#pragma unroll
+  for (int j = 0; j < NV; j += 4) {
+    if (wide && first + j < E) {
+      *reinterpret_cast<float4*>(row + first + j) = *reinterpret_cast<const float4*>(x + j);
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 4; ++i)
+        if (first + i < E) row[first + i] = x[i];
+    }
+  }
+}
+template <int NV>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int first, int E, bool wide,
+                                          const float* x) {
+#pragma unroll
+  for (int j = 0; j < NV; j += 8) {
+    if (wide && first + j < E) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[j + i];
+      *reinterpret_cast<uint4*>(row + first + j) = pack_bf16(v);
+    } else {
+#pragma unroll
+      for (int i = j; i < j + 8; ++i)
+        if (first + i < E) row[first + i] = __float2bfloat16_rn(x[i]);
+    }
+  }
+}
+
+// Reductions over the G lanes of a group (mask: those lanes of the warp).
+template <int G>
+__device__ __forceinline__ float group_sum(uint32_t mask, float v) {
+#pragma unroll
+  for (int d = G / 2; d > 0; d >>= 1) v += __shfl_xor_sync(mask, v, d);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int G>
+__device__ __forceinline__ float group_max(uint32_t mask, float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, d));
+  for (int d = G / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, d));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t mask, uint32_t v) {
+  if constexpr (G == 32) {
+    return __reduce_max_sync(mask, v);
+  } else {
+#pragma unroll
+    for (int d = G / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(mask, v, d));
+    return v;
+  }
+}
+template <int G>
+__device__ __forceinline__ uint64_t group_max(uint32_t mask, uint64_t v) {
+#pragma unroll
+  for (int d = G / 2; d > 0; d >>= 1) {
+    const uint64_t o = __shfl_xor_sync(mask, v, d);
+    v = o > v ? o : v;
+  }
   return v;
 }
 
@@ -56,14 +142,6 @@ __device__ __forceinline__ uint64_t key_of(double v) {
   const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
   return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
 }
-__device__ __forceinline__ uint32_t warp_max_key(uint32_t k) { return __reduce_max_sync(ALL, k); }
-__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
-  const uint32_t hi = __reduce_max_sync(ALL, (uint32_t)(k >> 32));
-  const uint32_t lo = __reduce_max_sync(ALL, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
-  return ((uint64_t)hi << 32) | lo;
-}
-template <bool BIAS> struct KeyOf { using type = uint32_t; };
-template <> struct KeyOf<true> { using type = uint64_t; };
 
 // A logit that can be chosen is finite. -inf is the mask; NaN and +inf are reported and then
 // treated as masked.
@@ -81,25 +159,198 @@ __device__ __forceinline__ float sigmoid_over(float x, float m) {
   return expf(fminf(x, 0.f) - m) / (1.f + expf(-fabsf(x)));
 }
 
-// Shares of the k chosen (lane s: slot s): softmax or sigmoid scores over their sum.
-__device__ __forceinline__ float share(bool live, float x, bool sigmoid) {
-  const float at = live ? (sigmoid ? fminf(x, 0.f) : x) : -INFINITY;
-  const float m = warp_max(at);
-  float v = 0.f;
-  if (live) v = sigmoid ? sigmoid_over(x, m) : expf(x - m);
-  const float total = warp_sum(v);
-  return live ? v / total : 0.f;
+// The score that a biased choice tries first. In units of 2^-23 it is off by at most
+// sigma (1 - sigma) (2 + 1.17 |x|) < 0.6 from the fast exponential, 2.5 from the sum and the
+// quotient and (1 + |bias|) / 2 from the last sum; two scores further apart than CLOSE
+// (1 + |bias| + |bias'|) are in the right order, with half of CLOSE to spare.
+__device__ __forceinline__ float fast_score(float x, float b) {
+  return __fdividef(1.f, 1.f + __expf(-x)) + b;
+}
+constexpr float CLOSE = 16.f / 8388608.f;
+
+struct Chosen {  // of one token, in shared memory
+  int32_t id[GG_GATE_MAX_K + 1];
+  float x[GG_GATE_MAX_K + 1];
+  float score[GG_GATE_MAX_K + 1];
+};
+
+// The `want` largest keys of the group, in order, ties to the lowest expert (the lowest lane,
+// and there the lowest place, as lanes hold neighbouring experts). Returns how many there are.
+template <int G, int NV>
+__device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_t (&key)[NV],
+                                      const float (&x)[NV], Chosen& c) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+  for (int s = 0; s < want; ++s) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) best = max(best, key[j]);
+    const uint32_t top = group_max<G>(mask, best);
+    if (top == 0) return s;  // nothing left
+    const uint32_t holders = __ballot_sync(mask, best == top);
+    if (best == top && (holders & below) == 0) {
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (!found && key[j] == top) {
+          found = true;
+          key[j] = 0;
+          c.id[s] = lane * NV + j;
+          c.x[s] = x[j];
+        }
+      }
+    }
+  }
+  return want;
+}
+
+// The same by double scores, for the few tokens whose fp32 scores do not decide: a function of
+// its own with the keys in local memory, so that it costs the others no registers.
+template <typename L, int G, int NV>
+__device__ __noinline__ int choose_double(uint32_t mask, int lane, int want, const L* row,
+                                          const float* bias, int E, Chosen* c) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+  uint64_t key[NV];
+#pragma unroll 1
+  for (int j = 0; j < NV; ++j) {
+    const int e = lane * NV + j;
+    key[j] = 0;
+    if (e >= E) continue;
+    bool ignored = false;
+    const float x = logit_or_mask(to_float(row[e]), &ignored);
+    const float b = logit_or_mask(bias[e], &ignored);
+    if (x > -INFINITY && b > -INFINITY) key[j] = key_of(1.0 / (1.0 + exp(-(double)x)) + (double)b);
+  }
+  for (int s = 0; s < want; ++s) {
+    uint64_t best = 0;
+    int at = 0;
+#pragma unroll 1
+    for (int j = 0; j < NV; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+      }
+    const uint64_t top = group_max<G>(mask, best);
+    if (top == 0) return s;
+    const uint32_t holders = __ballot_sync(mask, best == top);
+    if (best == top && (holders & below) == 0) {
+      key[at] = 0;
+      c->id[s] = lane * NV + at;
+      c->x[s] = to_float(row[lane * NV + at]);
+    }
+  }
+  return want;
+}
+
+// bf16 logits: value and expert fit one 32-bit key, 16 bits that grow with the value over the
+// complement of the expert's number, so that the largest key names its expert and ties resolve
+// by themselves. Each lane sorts its keys once; a round compares only the lanes' first keys and
+// moves the winner's up. NaN and +inf have the largest keys (or the smallest), so the first and
+// the last of the sorted show whether a lane has any. x: the logits in fp32.
+constexpr uint32_t KEY_INF = 0xff800000u;     // of +inf
+constexpr uint32_t KEY_LOWEST = 0x00800000u;  // of the lowest finite number
+constexpr uint32_t KEY_MASKED = 0x007f0000u;  // of -inf; a NaN with its sign set is below
+
+template <int NV>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
+  // Batcher's odd-even merge sort, largest first
+#pragma unroll
+  for (int p = 1; p < NV; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < NV; j += 2 * q)
+#pragma unroll
+        for (int i = j; i < j + q && i + q < NV; ++i)
+          if (i / (2 * p) == (i + q) / (2 * p)) {
+            const uint32_t hi = max(key[i], key[i + q]), lo = min(key[i], key[i + q]);
+            key[i] = hi;
+            key[i + q] = lo;
+          }
+}
+
+template <int G, int NV>
+__device__ __forceinline__ int choose_bf16(uint32_t mask, int lane, int want,
+                                           const __nv_bfloat16* row, int E, bool wide,
+                                           float (&x)[NV], Chosen& c, bool* bad) {
+  const int first = lane * NV;
+  uint32_t w[NV / 2];  // two logits each
+#pragma unroll
+  for (int j = 0; j < NV / 2; j += 4) {
+    if (NV >= 8 && wide && first + 2 * j < E) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + first + 2 * j);
+      w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
+    } else {
+      const unsigned short* bits = reinterpret_cast<const unsigned short*>(row);
+#pragma unroll
+      for (int i = j; i < j + 4 && i < NV / 2; ++i) {
+        const int e = first + 2 * i;
+        w[i] = (e < E ? bits[e] : 0xff80u) | (uint32_t)(e + 1 < E ? bits[e + 1] : 0xff80u) << 16;
+      }
+    }
+  }
+  uint32_t key[NV];
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < NV / 2; ++i) {
+    // + 0 turns -0 into +0; a negative number's 16 bits are complemented, a positive one's top
+    // bit is set
+    const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), zero);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    const uint32_t k = u ^ (((u >> 15) & 0x00010001u) * 0xffffu | 0x80008000u);
+    const uint32_t number = GG_MAX_EXPERTS - 1 - (first + 2 * i);
+    key[2 * i] = (k << 16) | number;
+    key[2 * i + 1] = (k & 0xffff0000u) | (number - 1);
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+#pragma unroll 1
+  for (int again = 0;; ++again) {
+    sort_keys(key);
+    const bool odd = key[0] >= KEY_INF || key[NV - 1] < KEY_MASKED;
+    if (again || !__any_sync(mask, odd)) break;  // almost always
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (key[j] >= KEY_INF) key[j] = 0;
+      x[j] = logit_or_mask(x[j], bad);
+    }
+  }
+  for (int s = 0; s < want; ++s) {
+    const uint32_t top = group_max<G>(mask, key[0]);
+    if (top < KEY_LOWEST) return s;  // only masked ones left
+    const bool won = key[0] == top;  // one lane: the keys differ
+#pragma unroll
+    for (int j = 0; j + 1 < NV; ++j) key[j] = won ? key[j + 1] : key[j];
+    key[NV - 1] = won ? 0u : key[NV - 1];
+    if (won) {
+      const uint32_t v = top & 0xffff0000u;
+      c.id[s] = GG_MAX_EXPERTS - 1 - (int)(top & 0xffffu);
+      c.x[s] = __uint_as_float((v >> 31) ? v ^ 0x80000000u : v ^ 0xffff0000u);
+    }
+  }
+  return want;
+}
+
+template <int G>
+__device__ __forceinline__ uint32_t group_mask() {
+  return G == 32 ? ALL : ((1u << (G & 31)) - 1u) << ((threadIdx.x & 31) / G * G);
 }
 
 // Choice by the logit itself without a bias (both scores grow with it, so the choice is
 // exact), by sigma(x) + bias in double precision with one: neighbours of 256 scores are often
-// closer than fp32 tells apart. Ties go to the lowest index.
-template <typename L, int NV, bool BIAS>
-__global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, bool renorm) {
-  using Key = typename KeyOf<BIAS>::type;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-  if (t >= p.T) return;
+// closer than fp32 tells apart. With a bias fp32 scores come first, one place further than
+// needed: only a token with two neighbours in that order within CLOSE of one another (other
+// than the same logit under the same bias, a tie in any precision; at the last place any two,
+// as others may lie behind them) is chosen again in double precision.
+template <typename L, int G, int NV, bool BIAS>
+__global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, bool renorm,
+                                                       bool wide, bool wide_bias) {
+  __shared__ Chosen chosen[THREADS / G];
+  const int lane = threadIdx.x % G;
+  const int64_t t = (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G;
+  if (t >= p.T) return;  // the whole group
+  const uint32_t mask = group_mask<G>();
+  Chosen& c = chosen[threadIdx.x / G];
+  const L* row = static_cast<const L*>(p.logits) + t * p.E;
   bool bad_count = false, bad = false;
   int64_t live_tokens = p.T;
   if (p.num_tokens != nullptr) {
@@ -107,71 +358,82 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
     bad_count = live_tokens < 0 || live_tokens > p.T;
   }
   float x[NV];
-  Key key[NV];
+  int got = 0;
+  if (t < live_tokens) {
+    if constexpr (!BIAS && sizeof(L) == 2) {
+      got = choose_bf16<G, NV>(mask, lane, p.k, row, p.E, wide, x, c, &bad);
+    } else {
+      load_row<NV>(row, lane * NV, p.E, wide, x);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = lane + 32 * j;
-    x[j] = -INFINITY;
-    if (c < p.E && t < live_tokens)
-      x[j] = logit_or_mask(load(static_cast<const L*>(p.logits) + t * p.E + c), &bad);
-    key[j] = 0;
-    if (x[j] > -INFINITY) {
+      for (int j = 0; j < NV; ++j) x[j] = logit_or_mask(x[j], &bad);
+      uint32_t key[NV];
       if constexpr (BIAS) {
-        const float b = p.bias[c];
-        if (!(b < INFINITY)) bad = true;
-        else if (b > -INFINITY) key[j] = key_of(1.0 / (1.0 + exp(-(double)x[j])) + (double)b);
+        float b[NV];
+        load_row<NV>(p.bias, lane * NV, p.E, wide_bias, b);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (x[j] > -INFINITY) b[j] = logit_or_mask(b[j], &bad);
+          const bool in = x[j] > -INFINITY && b[j] > -INFINITY;
+          key[j] = in ? key_of(fast_score(x[j], b[j])) : 0u;
+        }
+        got = choose<G, NV>(mask, lane, min(p.k + 1, p.E), key, x, c);
+        __syncwarp(mask);
+        bool undecided = false;
+        for (int s = lane; s + 1 < got; s += G) {
+          const float xa = c.x[s], xb = c.x[s + 1];
+          const float ba = p.bias[c.id[s]], bb = p.bias[c.id[s + 1]];
+          const float gap = fast_score(xa, ba) - fast_score(xb, bb);
+          undecided |= gap <= CLOSE * (1.f + fabsf(ba) + fabsf(bb)) &&
+                       (s + 1 == p.k || !(xa == xb && ba == bb));
+        }
+        if (__any_sync(mask, undecided))
+          got = choose_double<L, G, NV>(mask, lane, p.k, row, p.bias, p.E, &c);
+        got = min(got, p.k);
       } else {
-        key[j] = key_of(x[j]);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) key[j] = x[j] > -INFINITY ? key_of(x[j]) : 0u;
+        got = choose<G, NV>(mask, lane, p.k, key, x, c);
       }
     }
+    __syncwarp(mask);
   }
-  int32_t my_id = -1;
-  float my_x = -INFINITY;
-  for (int s = 0; s < p.k; ++s) {
-    Key best = 0;
-    int at = 0;
-    float bx = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = j;
-        bx = x[j];
-      }
-    const Key top = warp_max_key(best);
-    if (top == 0) break;  // nothing left to choose
-    const uint32_t c = __reduce_min_sync(ALL, best == top ? (uint32_t)(lane + 32 * at) : ALL);
-    const float cx = __shfl_sync(ALL, bx, c & 31);
-    if (lane == s) {
-      my_id = (int32_t)c;
-      my_x = cx;
+  float m = 0.f, total = 1.f;
+  if (got > 0 && (renorm || !sigmoid)) {
+    // shares: each score over the sum of the chosen (renorm) or of all (softmax), both relative
+    // to the largest
+    m = sigmoid ? -INFINITY : c.x[0];
+    if (sigmoid) {
+      for (int s = lane; s < got; s += G) m = fmaxf(m, fminf(c.x[s], 0.f));
+      m = group_max<G>(mask, m);
     }
+    total = 0.f;
+    if constexpr (!BIAS) {  // a biased gate is a sigmoid
+      if (!renorm) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (c == (uint32_t)(lane + 32 * j)) key[j] = 0;
+        for (int j = 0; j < NV; ++j) total += expf(x[j] - m);  // 0 of -inf
+      }
+    }
+    if (renorm) {
+      for (int s = lane; s < got; s += G) {
+        const float v = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
+        c.score[s] = v;
+        total += v;
+      }
+    }
+    total = group_sum<G>(mask, total);
   }
-  const bool live = my_id >= 0;
-  float w;
-  if (renorm) {
-    w = share(live, my_x, sigmoid);
-  } else if (sigmoid) {
-    w = live ? sigmoid_over(my_x, 0.f) : 0.f;
-  } else {
-    const float m = __shfl_sync(ALL, my_x, 0);
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (x[j] > -INFINITY) sum += expf(x[j] - m);
-    sum = warp_sum(sum);
-    w = live ? expf(my_x - m) / sum : 0.f;
+  for (int s = lane; s < p.k; s += G) {
+    float w = 0.f;
+    if (s < got) {
+      if (renorm) w = c.score[s];
+      else w = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
+      w = p.scale * __fdividef(w, total);
+    }
+    p.ids[t * p.k + s] = s < got ? c.id[s] : -1;
+    p.weights[t * p.k + s] = w;
   }
-  if (lane < p.k) {
-    p.ids[t * p.k + lane] = my_id;
-    p.weights[t * p.k + lane] = live ? p.scale * w : 0.f;
-  }
-  bad = __any_sync(ALL, bad);
-  if (lane == 0 && (bad || (bad_count && t == 0)))
-    flag(p.status, (bad ? GG_DEV_BAD_LOGIT : 0u) | (bad_count ? GG_DEV_BAD_COUNT : 0u));
+  if (bad) flag(p.status, GG_DEV_BAD_LOGIT);
+  if (bad_count && t == 0 && lane == 0) flag(p.status, GG_DEV_BAD_COUNT);
 }
 
 // Gradient of the logits. With v the weights before `scale` and g = scale * dweights:
@@ -179,96 +441,158 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 //   softmax renormalised  dx_i = v_i (g_i - sum g v)
 //   sigmoid               dx_i = g_i s_i (1 - s_i)
 //   sigmoid renormalised  dx_i = v_i (1 - s_i) (g_i - sum g v)
-// The chosen slots' scores are computed again from their logits; dx of a logit that was not
-// chosen is 0 but for the first form. A slot of id -1 carries nothing.
-template <typename L, int NV>
+// The scores are computed again from the logits; dx of a logit that was not chosen is 0 but for
+// the first form. A slot of id -1 carries nothing. A row in shared memory brings the slots to
+// their experts' lanes: it takes g (first form) or dx (the others), slot after slot, so that
+// slots of the same expert add up in their order.
+template <typename L, int G, int NV>
 __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool sigmoid,
-                                                                bool renorm) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-  if (t >= p.T) return;
+                                                                bool renorm, bool wide) {
+  __shared__ Chosen chosen[THREADS / G];
+  // four experts of every lane side by side, then the next four: lanes' vectors are neighbours;
+  // 16 floats more put the rows of two 4-lane groups into different banks
+  __shared__ __align__(16) float rows[THREADS / G][G * NV + 16];
+  const int lane = threadIdx.x % G;
+  const int64_t t = (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G;
+  if (t >= p.T) return;  // the whole group
+  const uint32_t mask = group_mask<G>();
+  Chosen& c = chosen[threadIdx.x / G];  // each lane reads only its own slots
+  float* d = rows[threadIdx.x / G];
   const L* row = static_cast<const L*>(p.logits) + t * p.E;
-  L* drow = static_cast<L*>(p.dlogits) + t * p.E;
-  int32_t id = -1;
-  float g = 0.f, x = -INFINITY;
+  const bool full = !sigmoid && !renorm;
+  float x[NV];
+  if (full) load_row<NV>(row, lane * NV, p.E, wide, x);
+#pragma unroll
+  for (int j = 0; j < NV / 4; ++j)
+    *reinterpret_cast<float4*>(d + (j * G + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false;
-  if (lane < p.k) {
-    id = p.ids[t * p.k + lane];
+  float m = -INFINITY;
+  for (int s = lane; s < p.k; s += G) {
+    int32_t id = p.ids[t * p.k + s];
     if (id >= p.E) {
       bad = true;
       id = -1;
     }
+    float g = 0.f;
     if (id >= 0) {
       bool ignored = false;
-      x = logit_or_mask(load(row + id), &ignored);
-      if (x > -INFINITY) g = p.scale * p.dweights[t * p.k + lane];
+      const float xs = logit_or_mask(to_float(row[id]), &ignored);
+      if (xs > -INFINITY) {
+        g = p.scale * p.dweights[t * p.k + s];
+        m = fmaxf(m, sigmoid ? fminf(xs, 0.f) : xs);
+        c.x[s] = xs;
+      } else {
+        id = -1;
+      }
+    }
+    c.id[s] = id;
+    c.score[s] = g;
+  }
+  m = group_max<G>(mask, m);
+  if (m > -INFINITY) {  // some slot carries something
+    if (!full) {
+      float total = 0.f, mean = 0.f;
+      for (int s = lane; s < p.k; s += G) {
+        if (c.id[s] < 0) continue;
+        const float v = renorm ? (sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m))
+                               : sigmoid_over(c.x[s], 0.f);
+        total += v;
+        mean = fmaf(c.score[s], v, mean);
+      }
+      total = renorm ? group_sum<G>(mask, total) : 1.f;
+      mean = renorm ? group_sum<G>(mask, mean) / total : 0.f;
+      for (int s = lane; s < p.k; s += G) {
+        if (c.id[s] < 0) continue;
+        const float xs = c.x[s];
+        float v = renorm ? (sigmoid ? sigmoid_over(xs, m) : expf(xs - m)) / total
+                         : sigmoid_over(xs, 0.f);
+        if (sigmoid) v *= sigmoid_over(-xs, 0.f);  // 1 - sigma(x) = sigma(-x)
+        c.score[s] = v * (c.score[s] - mean);
+      }
+    }
+    __syncwarp(mask);
+    for (int s = 0; s < p.k; ++s) {
+      if (s % G == lane) {
+        const int id = c.id[s];
+        // expert id is place i of lane id / NV
+        if (id >= 0) {
+          const int i = id % NV;
+          d[((i / 4) * G + id / NV) * 4 + i % 4] += c.score[s];
+        }
+      }
+      __syncwarp(mask);
     }
   }
-  const bool live = x > -INFINITY;
-  const bool any = __any_sync(ALL, live);
-  float all[NV];  // softmax over all: the row's logits, then its probabilities
-  float mine = 0.f, others = 0.f, m = 0.f, inv = 0.f;
-  if (!sigmoid && !renorm) {
-    float top = -INFINITY;
+  float out[NV];
+#pragma unroll
+  for (int j = 0; j < NV / 4; ++j) {
+    const float4 v = *reinterpret_cast<const float4*>(d + (j * G + lane) * 4);
+    out[4 * j] = v.x, out[4 * j + 1] = v.y, out[4 * j + 2] = v.z, out[4 * j + 3] = v.w;
+  }
+  if (full && m > -INFINITY) {
+    bool ignored = false;
+    float top = -INFINITY, total = 0.f, mean = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) top = fmaxf(top, x[j] = logit_or_mask(x[j], &ignored));
+    top = group_max<G>(mask, top);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = lane + 32 * j;
-      bool ignored = false;
-      all[j] = c < p.E && any ? logit_or_mask(load(row + c), &ignored) : -INFINITY;
-      top = fmaxf(top, all[j]);
+      x[j] = x[j] > -INFINITY ? expf(x[j] - top) : 0.f;
+      total += x[j];
+      mean = fmaf(x[j], out[j], mean);
     }
-    m = any ? warp_max(top) : 0.f;
-    float sum = 0.f;
+    const float inv = 1.f / group_sum<G>(mask, total);
+    mean = group_sum<G>(mask, mean) * inv;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      all[j] = all[j] > -INFINITY ? expf(all[j] - m) : 0.f;
-      sum += all[j];
-    }
-    sum = warp_sum(sum);
-    inv = any ? 1.f / sum : 0.f;
-    const float v = live ? expf(x - m) * inv : 0.f;
-    others = warp_sum(g * v);
-    mine = g * v;
-  } else if (renorm) {
-    const float v = share(live, x, sigmoid);
-    const float mean = warp_sum(g * v);
-    mine = live ? v * (g - mean) : 0.f;
-    if (sigmoid && live) mine *= sigmoid_over(-x, 0.f);  // 1 - sigma(x) = sigma(-x)
-  } else if (live) {
-    mine = g * sigmoid_over(x, 0.f) * sigmoid_over(-x, 0.f);
+    for (int j = 0; j < NV; ++j) out[j] = x[j] * inv * (out[j] - mean);
   }
-  float d[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) d[j] = !sigmoid && !renorm ? -others * (all[j] * inv) : 0.f;
-  for (int s = 0; s < p.k; ++s) {
-    const int c = __shfl_sync(ALL, id, s);
-    const float v = __shfl_sync(ALL, mine, s);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (c == lane + 32 * j) d[j] += v;
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (lane + 32 * j < p.E) store(drow + lane + 32 * j, d[j]);
+  store_row<NV>(static_cast<L*>(p.dlogits) + t * p.E, lane * NV, p.E, wide, out);
   if (bad) flag(p.status, GG_DEV_BAD_ROUTE);
 }
 
+template <int N> using Int = std::integral_constant<int, N>;
+
+// Lanes a token and experts a lane. A warp for each token is the quickest for few of them, NV
+// experts a lane and so more tokens a warp the cheapest in instructions for many.
+template <int NV, typename F>
+void by_experts(int E, bool few, const F& f) {
+  if (few && E <= 64) f(Int<32>(), Int<2>());
+  else if (few && E <= 128) f(Int<32>(), Int<4>());
+  else if (few && E <= 256) f(Int<32>(), Int<8>());
+  else if (E <= 64) f(Int<64 / NV>(), Int<NV>());
+  else if (E <= 128) f(Int<128 / NV>(), Int<NV>());
+  else if (E <= 256) f(Int<256 / NV>(), Int<NV>());
+  else if (E <= 512) f(Int<32>(), Int<16>());
+  else f(Int<32>(), Int<32>());
+}
+
+// 1 x 64 bf16: 2.4 us a call in a graph with a warp a token, 3.3 us with four lanes; 32768 x
+// 64: 16.2 and 7.7 us. The two break even where the warps fill the GPU (148 SMs x 32 or so).
+constexpr int64_t FEW = 4096;
+
 template <typename L, bool BIAS>
 void launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((p.T + WARPS - 1) / WARPS);
-  const int nv = (p.E + 31) / 32;
-  if (nv <= 2) gate_kernel<L, 2, BIAS><<<grid, THREADS, 0, stream>>>(p, sigmoid, renorm);
-  else if (nv <= 8) gate_kernel<L, 8, BIAS><<<grid, THREADS, 0, stream>>>(p, sigmoid, renorm);
-  else gate_kernel<L, 32, BIAS><<<grid, THREADS, 0, stream>>>(p, sigmoid, renorm);
+  const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16);
+  const bool wide_bias = p.E % 8 == 0 && !misaligned(p.bias, 16);
+  // sorted keys take sixteen experts a lane well (8: 8.8 us for 32768 x 64), the fp32 search,
+  // which looks through a lane's keys in each round, eight (16411 x 256 with a bias: 22.6 us,
+  // 28.1 with sixteen)
+  constexpr int MANY = !BIAS && sizeof(L) == 2 ? 16 : 8;
+  by_experts<MANY>(p.E, p.T <= FEW, [&](auto g, auto nv) {
+    constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
+    gate_kernel<L, G, NV, BIAS><<<(unsigned)((p.T + PER - 1) / PER), THREADS, 0, stream>>>(
+        p, sigmoid, renorm, wide, wide_bias);
+  });
 }
 
 template <typename L>
 void launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((p.T + WARPS - 1) / WARPS);
-  const int nv = (p.E + 31) / 32;
-  if (nv <= 2) gate_backward_kernel<L, 2><<<grid, THREADS, 0, stream>>>(p, sigmoid, renorm);
-  else if (nv <= 8) gate_backward_kernel<L, 8><<<grid, THREADS, 0, stream>>>(p, sigmoid, renorm);
-  else gate_backward_kernel<L, 32><<<grid, THREADS, 0, stream>>>(p, sigmoid, renorm);
+  const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16) && !misaligned(p.dlogits, 16);
+  by_experts<16>(p.E, false, [&](auto g, auto nv) {
+    constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
+    gate_backward_kernel<L, G, NV><<<(unsigned)((p.T + PER - 1) / PER), THREADS, 0, stream>>>(
+        p, sigmoid, renorm, wide);
+  });
 }
 
 gg_status check(int64_t T, int32_t E, int32_t k, int32_t score, int32_t flags, float scale,

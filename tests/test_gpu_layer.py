@@ -145,8 +145,16 @@ def test_gate_flags_bad_logits_and_counts():
     x = torch.randn(6, 16, generator=torch.Generator().manual_seed(2))
     x[1, 3] = float("nan")
     x[2, 0] = float("inf")
-    _check_gate(x, 4, False, True, 1.0, flagged=gg.DEV_BAD_LOGIT)
-    _check_gate(x, 4, True, False, 1.0, flagged=gg.DEV_BAD_LOGIT)
+    x[3, 7] = torch.tensor([-1], dtype=torch.int32).view(torch.float32)[0]  # NaN, sign set
+    for z in (x, x.to(torch.bfloat16)):
+        for renorm in (False, True):
+            _check_gate(z, 4, False, renorm, 1.0, flagged=gg.DEV_BAD_LOGIT)
+            _check_gate(z, 4, True, renorm, 1.0, flagged=gg.DEV_BAD_LOGIT)
+    z = x.to(torch.bfloat16)
+    z[3, 7], z[1, 3], z[2, 0] = 0.0, 1.0, 2.0
+    z.view(torch.int16)[3, 7] = -1
+    _check_gate(z, 4, False, False, 1.0, flagged=gg.DEV_BAD_LOGIT)
+    x[3, 7] = 0.5
     bias = torch.zeros(16)
     bias[5] = float("nan")
     bias[6] = -float("inf")  # a mask, as such no error
@@ -171,6 +179,23 @@ def test_gate_bias_decides_close_calls():
     want = torch.sigmoid(x[0].double())
     bias = (0.7 - want).float()  # every sum of token 0 lies within 2^-25 of 0.7
     _check_gate(x, 8, True, True, 1.0, bias=bias)
+
+
+@pytest.mark.parametrize("E,k", [(33, 8), (64, 6), (200, 8), (300, 4), (1000, 32)])
+def test_gate_neighbours_and_ties(E, k):
+    """Logits that differ in their last bits only, logits of few distinct values, and biases of
+    0: the order is that of the values, ties to the lowest expert."""
+    gen = torch.Generator().manual_seed(E)
+    near = 1.0 + torch.randint(0, 64, (40, E), generator=gen).float() * 2.0 ** -23
+    few = torch.randint(-3, 4, (40, E), generator=gen).float()
+    one = few.clone()
+    one[:, E // 2:] = near[:, E // 2:]
+    for x in (near, few, one, -near):
+        _check_gate(x, k, False, True, 1.0)
+        _check_gate(x, k, True, False, 1.0, bias=torch.zeros(E))
+        _check_gate(x, k, True, True, 1.0, bias=0.125 * torch.randint(-1, 2, (E,), generator=gen))
+    _check_gate(few.to(torch.bfloat16), k, False, False, 1.0)
+    _check_gate(few.to(torch.bfloat16), k, True, True, 1.0, bias=torch.zeros(E))
 
 
 # ----------------------------------------------------------------------------- unroute
