@@ -30,85 +30,149 @@ struct Params {
   int32_t k;
 };
 
-// Packed row of an assignment: -1 when it was dropped or names no row.
-__device__ __forceinline__ int64_t row_at(const Params& p, int64_t i, int64_t rows,
-                                          bool report) {
-  const int64_t r = p.row_of[i];
-  if (r >= rows) {
-    if (report) flag(p.status, GG_DEV_BAD_ROUTE);
-    return -1;
-  }
-  return r < 0 ? -1 : r;
-}
+// Both kernels are held to 64 registers: four blocks an SM keep 128 KB of 16-byte loads in
+// flight, which the memory needs. us for 4096 tokens x 8 slots of 2048 columns, and 32768 x 8 of
+// 6144: forward 24 and 541 (the bytes at the copy rate: 23 and 562), 28 and 661 with three
+// blocks, 33 and 658 with five (spills); backward of the former 48 (44), 51 with three, 63 with
+// five.
+constexpr int BLOCKS = 4;
+constexpr int SLOTS = 8;  // slots taken at once: as many 16-byte loads in flight per thread
 
-__global__ void __launch_bounds__(THREADS) unroute_kernel(Params p) {
-  const int64_t t = blockIdx.x;
-  for (int64_t v = threadIdx.x; v < p.vecs; v += THREADS) {
-    float acc[8] = {};
-    for (int s = 0; s < p.k; ++s) {
-      const int64_t r = row_at(p, t * p.k + s, p.rows, v == 0);
-      if (r < 0) continue;
-      const float w = p.weights != nullptr ? p.weights[t * p.k + s] : 1.f;
-      float y[8];
-      unpack_bf16(p.Y[r * p.vecs + v], y);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, y[i], acc[i]);
+// Rows and weights of SLOTS slots of token t, from slot s0 on: negative and 0 for a dropped
+// assignment or one past `rows`. Each lane fetches one slot, the warp shares them. Called by
+// whole warps.
+__device__ __forceinline__ void slots_of(const Params& p, int64_t t, int s0, int64_t rows,
+                                         bool report, int32_t (&r)[SLOTS], float (&w)[SLOTS]) {
+  const int s = s0 + (threadIdx.x & (SLOTS - 1));
+  int32_t row = -1;  // negative: dropped
+  float weight = 0.f;
+  if (s < p.k) {
+    row = p.row_of[t * p.k + s];
+    if (row >= rows) {
+      if (report && (threadIdx.x & 31) < SLOTS) flag(p.status, GG_DEV_BAD_ROUTE);
+      row = -1;
     }
-    if (p.residual != nullptr) {
-      float y[8];
-      unpack_bf16(p.residual[t * p.vecs + v], y);
+    if (row >= 0) weight = p.weights != nullptr ? p.weights[t * p.k + s] : 1.f;
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += y[i];
-    }
-    p.out[t * p.vecs + v] = pack_bf16(acc);
+  for (int i = 0; i < SLOTS; ++i) {
+    r[i] = __shfl_sync(0xffffffffu, row, i);
+    w[i] = __shfl_sync(0xffffffffu, weight, i);
   }
 }
 
-// dY[r] = w dout[t] and dw = <dout[t], Y[r]> of every slot; blocks past the tokens write zeros
-// to the rows that are not in use.
-__global__ void __launch_bounds__(THREADS) unroute_backward_kernel(Params p) {
-  __shared__ float part[WARPS];
+// A block takes blockDim.x vectors of a token's columns; a thread's loads of all slots are in
+// flight together.
+__global__ void __launch_bounds__(THREADS, BLOCKS) unroute_kernel(Params p, int32_t chunks) {
+  const int64_t t = blockIdx.x / chunks;
+  const int32_t chunk = blockIdx.x % chunks;
+  const int64_t v = (int64_t)chunk * blockDim.x + threadIdx.x;
+  const bool in = v < p.vecs;
+  float acc[8] = {};
+  uint4 res = make_uint4(0, 0, 0, 0);
+  if (in && p.residual != nullptr) res = p.residual[t * p.vecs + v];
+  for (int s0 = 0; s0 < p.k; s0 += SLOTS) {
+    int32_t r[SLOTS];
+    float w[SLOTS];
+    slots_of(p, t, s0, p.rows, chunk == 0 && threadIdx.x < 32, r, w);
+    uint4 y[SLOTS];
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i)
+      if (in && r[i] >= 0) y[i] = __ldcs(p.Y + (int64_t)r[i] * p.vecs + v);  // read once
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      if (r[i] < 0) continue;
+      float x[8];
+      unpack_bf16(y[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(w[i], x[j], acc[j]);
+    }
+  }
+  if (!in) return;
+  if (p.residual != nullptr) {
+    float x[8];
+    unpack_bf16(res, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += x[j];
+  }
+  p.out[t * p.vecs + v] = pack_bf16(acc);
+}
+
+// Sums over the warp of eight values at once: each step halves the values a lane holds. Lane l
+// ends with the sum of value (l >> 2) & 7, its bits reversed (bit 4 of l is worth 4).
+__device__ __forceinline__ float warp_sums(float (&v)[SLOTS]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 4; n >= 1; n /= 2) {
+    const bool up = (lane & (4 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n];
+      v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, send, 4 * n);
+    }
+  }
+  float x = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return x + __shfl_xor_sync(0xffffffffu, x, 1);
+}
+
+// dY[r] = w dout[t] and dw = <dout[t], Y[r]> of every slot, one block a token; the blocks past
+// the tokens write zeros to the rows that are not in use.
+template <bool DY, bool DW>
+__global__ void __launch_bounds__(THREADS, BLOCKS) unroute_backward_kernel(Params p) {
+  __shared__ float part[WARPS][SLOTS];
   const int64_t used =
       rows_in_use(p.used, p.rows, p.status, blockIdx.x == 0 && threadIdx.x == 0);
   if (blockIdx.x >= p.T) {
-    const int64_t r = used + (blockIdx.x - p.T);
-    if (r >= p.rows) return;
-    for (int64_t v = threadIdx.x; v < p.vecs; v += THREADS)
-      p.dY[r * p.vecs + v] = make_uint4(0, 0, 0, 0);
+    for (int64_t r = used + (blockIdx.x - p.T); r < p.rows; r += gridDim.x - p.T)
+      for (int64_t v = threadIdx.x; v < p.vecs; v += blockDim.x)
+        p.dY[r * p.vecs + v] = make_uint4(0, 0, 0, 0);
     return;
   }
   const int64_t t = blockIdx.x;
-  for (int s = 0; s < p.k; ++s) {
-    const int64_t r = row_at(p, t * p.k + s, used, threadIdx.x == 0);
-    const float w = p.weights != nullptr ? p.weights[t * p.k + s] : 1.f;
-    float dot = 0.f;
-    if (r >= 0) {
-      for (int64_t v = threadIdx.x; v < p.vecs; v += THREADS) {
-        float d[8], y[8];
-        unpack_bf16(p.dout[t * p.vecs + v], d);
-        if (p.dweights != nullptr) {
-          unpack_bf16(p.Y[r * p.vecs + v], y);
+  for (int s0 = 0; s0 < p.k; s0 += SLOTS) {
+    int32_t r[SLOTS];
+    float w[SLOTS], dot[SLOTS] = {};
+    slots_of(p, t, s0, used, threadIdx.x < 32, r, w);
+    for (int64_t v = threadIdx.x; v < p.vecs; v += blockDim.x) {
+      const uint4 dv = p.dout[t * p.vecs + v];
+      uint4 y[SLOTS];
+      if constexpr (DW) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fmaf(d[i], y[i], dot);
+        for (int i = 0; i < SLOTS; ++i)
+          if (r[i] >= 0) y[i] = __ldcs(p.Y + (int64_t)r[i] * p.vecs + v);
+      }
+      float d[8];
+      unpack_bf16(dv, d);
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        if (r[i] < 0) continue;
+        float x[8];
+        if constexpr (DW) {
+          unpack_bf16(y[i], x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dot[i] = fmaf(d[j], x[j], dot[i]);
         }
-        if (p.dY != nullptr) {
+        if constexpr (DY) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] *= w;
-          p.dY[r * p.vecs + v] = pack_bf16(d);
+          for (int j = 0; j < 8; ++j) x[j] = w[i] * d[j];
+          p.dY[(int64_t)r[i] * p.vecs + v] = pack_bf16(x);
         }
       }
     }
-    if (p.dweights != nullptr) {
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float sum = 0.f;
-        for (int i = 0; i < WARPS; ++i) sum += part[i];
-        p.dweights[t * p.k + s] = sum;
+    if constexpr (DW) {
+      const int lane = threadIdx.x & 31;
+      const float sum = warp_sums(dot);
+      if ((lane & 3) == 0) {
+        const int i = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+        part[threadIdx.x >> 5][i] = sum;
       }
       __syncthreads();
+      if (threadIdx.x < SLOTS && s0 + threadIdx.x < p.k) {
+        float all = 0.f;
+        for (int i = 0; i < (int)blockDim.x / 32; ++i) all += part[i][threadIdx.x];
+        p.dweights[t * p.k + s0 + threadIdx.x] = all;
+      }
+      __syncthreads();  // part is written again for the next slots
     }
   }
 }
@@ -152,7 +216,10 @@ gg_status gg_unroute(const void* Y, int64_t rows, const int32_t* row_of, const f
   p.rows = rows;
   p.vecs = N / 8;
   p.k = k;
-  unroute_kernel<<<(unsigned)T_tok, THREADS, 0, stream>>>(p);
+  const int64_t chunks = (p.vecs + THREADS - 1) / THREADS;
+  if (T_tok * chunks >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
+  const unsigned threads = 32 * (unsigned)((p.vecs + 32 * chunks - 1) / (32 * chunks));
+  unroute_kernel<<<(unsigned)(T_tok * chunks), threads, 0, stream>>>(p, (int32_t)chunks);
   return launched("gg_unroute");
 }
 
@@ -176,7 +243,8 @@ gg_status gg_unroute_backward(const void* dout, const void* Y, int64_t rows,
   if (dY == nullptr && dweights == nullptr && rows > 0) return GG_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = device_sms(&sms)) != GG_OK) return s;
-  const int64_t grid = T_tok + (zero ? rows : 0);
+  const int64_t tail = !zero ? 0 : rows < 4 * sms ? rows : 4 * sms;  // blocks that clear rows
+  const int64_t grid = T_tok + tail;
   if (grid == 0) return GG_OK;
   if (grid >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
   Params p = {};
@@ -192,7 +260,14 @@ gg_status gg_unroute_backward(const void* dout, const void* Y, int64_t rows,
   p.rows = rows;
   p.vecs = N / 8;
   p.k = k;
-  unroute_backward_kernel<<<(unsigned)grid, THREADS, 0, stream>>>(p);
+  const int64_t rounds = (p.vecs + THREADS - 1) / THREADS;
+  const unsigned threads = 32 * (unsigned)((p.vecs + 32 * rounds - 1) / (32 * rounds));
+  if (dweights == nullptr)
+    unroute_backward_kernel<true, false><<<(unsigned)grid, threads, 0, stream>>>(p);
+  else if (dY == nullptr)
+    unroute_backward_kernel<false, true><<<(unsigned)grid, threads, 0, stream>>>(p);
+  else
+    unroute_backward_kernel<true, true><<<(unsigned)grid, threads, 0, stream>>>(p);
   return launched("gg_unroute_backward");
 }
 
