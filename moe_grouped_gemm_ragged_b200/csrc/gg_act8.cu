@@ -10,8 +10,16 @@ namespace act8 {
 
 using namespace gg::ops;
 
-constexpr int THREADS = 128;
+constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
+constexpr uint32_t ALL = 0xffffffffu;
+// Pieces of 32 vectors that a warp takes at once. 64 registers a thread (four blocks an SM) hold
+// four of them; the backward pass, with twice the values a piece, two. us for 65536 rows of
+// 4096 columns, forward and backward: 177 and 257 with four, 188 and 217 with two (the bytes at
+// the copy rate: 168 and 209); 262144 x 6144 to 8 bits and back: 807 and 817 with four, 867 and
+// 828 with two (764 each).
+constexpr int BLOCKS = 4;
+constexpr int MANY = 4, MANY_BACKWARD = 2;
 
 struct Params {
   const uint4* H;           // [rows, N] bf16
@@ -29,34 +37,58 @@ struct Params {
   int32_t* status;
   int64_t rows;
   int64_t n;                // assignments (with row_of) or rows
+  int64_t tail0;            // first block that only clears rows
   int32_t half;             // I = N / 2
   int32_t concat;
   int32_t zero_tail;
 };
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// sigma(x) = 1 / (1 + 2^(-x log2 e)) of a pair, by the hardware's powers and reciprocals: off by
+// 1 + |x| log2 e units of 2^-23 or so, against half a step of 2^-8 in the bf16 results. Numbers
+// below 2^-126 count as 0.
+__device__ __forceinline__ float2 sigmoid(const float2& x) {
+  float2 t = __fmul2_rn(x, both(-1.44269504f));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.y));
+  t = __fadd2_rn(t, both(1.f));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.y));
+  return t;
+}
 
-// What block b works on: a packed row with the index of its weight, a row to clear (weight
-// index -1), or nothing (row -1; the weight's gradient is then 0).
-struct Work {
-  int64_t row;
-  int64_t at;
-};
-__device__ __forceinline__ Work work_of(const Params& p, int64_t b) {
-  const bool report = threadIdx.x == 0;
-  if (p.row_of == nullptr) {
-    const int64_t used = rows_in_use(p.used, p.rows, p.status, report && b == 0);
-    if (b < used) return {b, b};
-    return {p.zero_tail ? b : -1, -1};
-  }
-  const int64_t used = rows_in_use(p.used, p.rows, p.status, report && b == 0);
-  if (b < p.n) {
-    const int64_t r = p.row_of[b];
-    if (r >= used && report) flag(p.status, GG_DEV_BAD_ROUTE);
-    return {r >= used || r < 0 ? -1 : r, b};
-  }
-  const int64_t r = used + (b - p.n);
-  return {r < p.rows ? r : -1, -1};
+// A row belongs to W warps of a block (1 or all), which take its 32-vector pieces in turn, U
+// pieces at once: their loads are in flight together.
+template <int W>
+__device__ __forceinline__ int64_t my_item() {
+  return (int64_t)blockIdx.x * (WARPS / W) + (threadIdx.x >> 5) / W;
+}
+template <int W, int U>
+__device__ __forceinline__ int first_vec() {
+  return (threadIdx.x >> 5) % W * U * 32 + (threadIdx.x & 31);
+}
+// One thread of the row's warps.
+template <int W>
+__device__ __forceinline__ bool leader() {
+  return threadIdx.x % (W * 32) == 0;
+}
+
+// Packed row of item b (an assignment, or a row), -1 for a dropped assignment; *live: the row
+// is in use. A row that may not be in use can be loaded from, as it is allocated, while *used
+// is still on its way.
+__device__ __forceinline__ int64_t row_of_item(const Params& p, int64_t b, int64_t used,
+                                               bool report) {
+  if (p.row_of == nullptr) return b;
+  const int64_t r = p.row_of[b];
+  if (r >= used && report) flag(p.status, GG_DEV_BAD_ROUTE);
+  return r >= used ? -1 : r;
+}
+
+// The blocks from tail0 on clear the rows of `out` (vecs vectors each) that are not in use.
+__device__ __forceinline__ void clear_tail(const Params& p, int64_t used, uint4* out, int vecs) {
+  const int64_t warps = (int64_t)(gridDim.x - p.tail0) * WARPS;
+  for (int64_t r = used + (blockIdx.x - p.tail0) * WARPS + (threadIdx.x >> 5); r < p.rows;
+       r += warps)
+    for (int c = threadIdx.x & 31; c < vecs; c += 32) out[r * vecs + c] = make_uint4(0, 0, 0, 0);
 }
 
 // Vector index of gate columns [8 c, 8 c + 8) in a row of H, and of the up columns beside
@@ -74,131 +106,229 @@ __device__ __forceinline__ int64_t up_code(const Params& p, int c) {
   return p.concat ? (c >> 2) + (p.half + kBlock - 1) / kBlock : gate_code(p, c) + 4;
 }
 
-__global__ void __launch_bounds__(THREADS) silu_mul_kernel(Params p) {
-  const Work w = work_of(p, blockIdx.x);
-  if (w.row < 0) return;
+template <int W, int U, bool CKPT>
+__global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
   const int vecs = p.half / 8;
-  if (w.at < 0) {
-    for (int c = threadIdx.x; c < vecs; c += THREADS)
-      p.act[w.row * vecs + c] = make_uint4(0, 0, 0, 0);
+  const int64_t used =
+      rows_in_use(p.used, p.rows, p.status, blockIdx.x == 0 && threadIdx.x == 0);
+  if (blockIdx.x >= p.tail0) {
+    clear_tail(p, used, p.act, vecs);
     return;
   }
-  const float scale = p.weights != nullptr ? p.weights[w.at] : 1.f;
-  const int64_t base = w.row * 2 * vecs;
-  const int64_t code0 = w.row * 2 * ((p.half + kBlock - 1) / kBlock);
+  const int64_t item = my_item<W>();
+  if (item >= p.n) return;
+  const int64_t row = row_of_item(p, item, used, leader<W>());
+  if (row < 0) return;
+  const int64_t base = row * 2 * vecs;
+  const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
+  const float scale = p.weights != nullptr ? p.weights[item] : 1.f;
   // whole warps go round together: the four lanes of a block exchange their largest values
-  for (int c = threadIdx.x; c - (int)(threadIdx.x & 31) < vecs; c += THREADS) {
-    float g[8] = {}, u[8] = {};
-    const bool in = c < vecs;
-    if (in) {
-      unpack_bf16(p.H[base + gate_vec(p, c)], g);
-      unpack_bf16(p.H[base + up_vec(p, c)], u);
-    }
-    if (p.H8_out != nullptr) {
-      const uint32_t cg = block_code(block_amax(amax_bits(g)));
-      const uint32_t cu = block_code(block_amax(amax_bits(u)));
-      if (in) {
-        p.H8_out[base + gate_vec(p, c)] = to_e4m3(g, cg);
-        p.H8_out[base + up_vec(p, c)] = to_e4m3(u, cu);
-        if ((c & 3) == 0) {
-          p.scale_out[code0 + gate_code(p, c)] = (uint8_t)cg;
-          p.scale_out[code0 + up_code(p, c)] = (uint8_t)cu;
-        }
+  for (int c0 = first_vec<W, U>(); c0 - (int)(threadIdx.x & 31) < vecs; c0 += W * U * 32) {
+    uint4 gv[U], uv[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i;
+      gv[i] = uv[i] = make_uint4(0, 0, 0, 0);
+      if (c < vecs) {
+        gv[i] = __ldcs(p.H + base + gate_vec(p, c));
+        uv[i] = __ldcs(p.H + base + up_vec(p, c));
       }
     }
-    if (in) {
-      float a[8];
+    if (row >= used) return;  // the whole warp
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = scale * (g[i] * sigmoid(g[i]) * u[i]);
-      p.act[w.row * vecs + c] = pack_bf16(a);
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i;
+      if (c - (int)(threadIdx.x & 31) >= vecs) break;  // the whole warp
+      float2 g[4], u[4];
+      unpack_bf16(gv[i], g);
+      unpack_bf16(uv[i], u);
+      if constexpr (CKPT) {
+        uint32_t cg, cu;
+        bool odd;
+        block_codes(gv[i], uv[i], cg, cu, &odd);
+        if (c < vecs) {
+          p.H8_out[base + gate_vec(p, c)] = to_e4m3(g, cg, odd);
+          p.H8_out[base + up_vec(p, c)] = to_e4m3(u, cu, odd);
+          if ((c & 3) == 0) {
+            p.scale_out[code0 + gate_code(p, c)] = (uint8_t)cg;
+            p.scale_out[code0 + up_code(p, c)] = (uint8_t)cu;
+          }
+        }
+      }
+      if (c < vecs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          g[j] = __fmul2_rn(__fmul2_rn(__fmul2_rn(g[j], sigmoid(g[j])), u[j]), both(scale));
+        p.act[row * vecs + c] = pack_bf16(g);
+      }
     }
   }
 }
 
 // h = [g, u] from its 8 bits (or bf16), s the row's weight, q = sigma(g):
-//   dg = s dact u q (1 + g (1 - q)),  du = s dact g q,  act = s g q u,  ds = <dact, g q u>
-__global__ void __launch_bounds__(THREADS) silu_mul_backward_kernel(Params p) {
+//   dg = s dact u (q + g q (1 - q)),  du = s dact g q,  act = s g q u,  ds = <dact, g q u>
+template <int W, int U, bool FROM8>
+__global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Params p) {
   __shared__ float part[WARPS];
-  const Work w = work_of(p, blockIdx.x);
   const int vecs = p.half / 8;
-  float dot = 0.f;
-  if (w.row >= 0) {
-    const int64_t base = w.row * 2 * vecs;
-    if (w.at < 0) {
-      for (int c = threadIdx.x; c < vecs; c += THREADS) {
-        p.dH[base + c] = p.dH[base + vecs + c] = make_uint4(0, 0, 0, 0);
-        if (p.act != nullptr) p.act[w.row * vecs + c] = make_uint4(0, 0, 0, 0);
-      }
-      return;
-    }
-    const float scale = p.weights != nullptr ? p.weights[w.at] : 1.f;
-    const int64_t code0 = w.row * 2 * ((p.half + kBlock - 1) / kBlock);
-    for (int c = threadIdx.x; c < vecs; c += THREADS) {
-      float g[8], u[8], d[8], a[8], dg[8], du[8];
-      if (p.H8 != nullptr) {
-        from_e4m3(p.H8[base + gate_vec(p, c)],
-                  code_scale(p.H8_scale[code0 + gate_code(p, c)]), g);
-        from_e4m3(p.H8[base + up_vec(p, c)], code_scale(p.H8_scale[code0 + up_code(p, c)]), u);
-      } else {
-        unpack_bf16(p.H[base + gate_vec(p, c)], g);
-        unpack_bf16(p.H[base + up_vec(p, c)], u);
-      }
-      unpack_bf16(p.dact[w.row * vecs + c], d);
+  const int64_t used =
+      rows_in_use(p.used, p.rows, p.status, blockIdx.x == 0 && threadIdx.x == 0);
+  if (blockIdx.x >= p.tail0) {
+    clear_tail(p, used, p.dH, 2 * vecs);
+    if (p.act != nullptr) clear_tail(p, used, p.act, vecs);
+    return;
+  }
+  const int64_t item = my_item<W>();
+  if (item >= p.n) return;
+  const int64_t row = row_of_item(p, item, used, leader<W>());
+  float2 dots = both(0.f);
+  if (row >= 0) {
+    const int64_t base = row * 2 * vecs;
+    const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
+    const float scale = p.weights != nullptr ? p.weights[item] : 1.f;
+    for (int c0 = first_vec<W, U>(); c0 < vecs; c0 += W * U * 32) {
+      uint4 gv[U], uv[U], dv[U];
+      uint2 g8[U], u8[U];
+      uint8_t cg[U], cu[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = sigmoid(g[i]), silu = g[i] * q, sd = scale * d[i];
-        dot = fmaf(d[i], silu * u[i], dot);
-        a[i] = scale * (silu * u[i]);
-        dg[i] = sd * u[i] * (q * (1.f + g[i] * (1.f - q)));
-        du[i] = sd * silu;
+      for (int i = 0; i < U; ++i) {
+        const int c = c0 + 32 * i;
+        if (c >= vecs) continue;
+        if constexpr (FROM8) {
+          g8[i] = __ldcs(p.H8 + base + gate_vec(p, c));
+          u8[i] = __ldcs(p.H8 + base + up_vec(p, c));
+          cg[i] = p.H8_scale[code0 + gate_code(p, c)];
+          cu[i] = p.H8_scale[code0 + up_code(p, c)];
+        } else {
+          gv[i] = __ldcs(p.H + base + gate_vec(p, c));
+          uv[i] = __ldcs(p.H + base + up_vec(p, c));
+        }
+        dv[i] = __ldcs(p.dact + row * vecs + c);
       }
-      p.dH[base + gate_vec(p, c)] = pack_bf16(dg);
-      p.dH[base + up_vec(p, c)] = pack_bf16(du);
-      if (p.act != nullptr) p.act[w.row * vecs + c] = pack_bf16(a);
+      if (row >= used) return;  // the row's warps together
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int c = c0 + 32 * i;
+        if (c >= vecs) continue;
+        float2 g[4], u[4], d[4], a[4];
+        if constexpr (FROM8) {
+          from_e4m3(g8[i], code_scale(cg[i]), g);
+          from_e4m3(u8[i], code_scale(cu[i]), u);
+        } else {
+          unpack_bf16(gv[i], g);
+          unpack_bf16(uv[i], u);
+        }
+        unpack_bf16(dv[i], d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 q = sigmoid(g[j]), silu = __fmul2_rn(g[j], q);
+          const float2 su = __fmul2_rn(silu, u[j]), sd = __fmul2_rn(d[j], both(scale));
+          dots = __ffma2_rn(d[j], su, dots);
+          a[j] = __fmul2_rn(su, both(scale));
+          // q + silu - silu q
+          const float2 slope =
+              __ffma2_rn(make_float2(-silu.x, -silu.y), q, __fadd2_rn(q, silu));
+          g[j] = __fmul2_rn(__fmul2_rn(sd, u[j]), slope);
+          u[j] = __fmul2_rn(sd, silu);
+        }
+        p.dH[base + gate_vec(p, c)] = pack_bf16(g);
+        p.dH[base + up_vec(p, c)] = pack_bf16(u);
+        if (p.act != nullptr) p.act[row * vecs + c] = pack_bf16(a);
+      }
     }
   }
-  if (p.dweights == nullptr || w.at < 0) return;  // the same for the whole block
+  // A row that is not in use (only without row_of) keeps its weight's gradient. A warp whose
+  // share of such a row is empty has not returned above; it may do so here, as all of its row's
+  // warps are past their loops or gone, and none of them reaches the barrier below.
+  if (p.dweights == nullptr || row >= used) return;
+  float dot = dots.x + dots.y;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float sum = 0.f;
-    for (int i = 0; i < WARPS; ++i) sum += part[i];
-    p.dweights[w.at] = sum;
+  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(ALL, dot, d);
+  if constexpr (W == 1) {
+    if ((threadIdx.x & 31) == 0) p.dweights[item] = dot;
+  } else {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float sum = 0.f;
+      for (int i = 0; i < WARPS; ++i) sum += part[i];
+      p.dweights[item] = sum;
+    }
   }
 }
 
-__global__ void __launch_bounds__(THREADS) pack8_kernel(const uint4* X, uint2* X8, uint8_t* scale,
-                                                        int64_t rows, int32_t vecs,
-                                                        const int32_t* used, int32_t* status) {
-  const int64_t r = blockIdx.x;
-  if (r >= rows_in_use(used, rows, status, r == 0 && threadIdx.x == 0)) return;
+template <int W, int U>
+__global__ void __launch_bounds__(THREADS, BLOCKS) pack8_kernel(
+    const uint4* X, uint2* X8, uint8_t* scale, int64_t rows, int32_t vecs, const int32_t* used,
+    int32_t* status) {
+  const int64_t n = rows_in_use(used, rows, status, blockIdx.x == 0 && threadIdx.x == 0);
+  const int64_t r = my_item<W>();
+  if (r >= rows) return;
   const int64_t codes = (vecs + 3) / 4;
-  for (int c = threadIdx.x; c - (int)(threadIdx.x & 31) < vecs; c += THREADS) {
-    float x[8] = {};
-    if (c < vecs) unpack_bf16(X[r * vecs + c], x);
-    const uint32_t code = block_code(block_amax(amax_bits(x)));
-    if (c < vecs) {
-      X8[r * vecs + c] = to_e4m3(x, code);
-      if ((c & 3) == 0) scale[r * codes + (c >> 2)] = (uint8_t)code;
+  for (int c0 = first_vec<W, U>(); c0 - (int)(threadIdx.x & 31) < vecs; c0 += W * U * 32) {
+    uint4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i;
+      v[i] = c < vecs ? __ldcs(X + r * vecs + c) : make_uint4(0, 0, 0, 0);
+    }
+    if (r >= n) return;
+    constexpr int P = U > 1 ? 2 : 1;  // pieces whose codes are found together
+#pragma unroll
+    for (int i = 0; i < U; i += P) {
+      if (c0 + 32 * i - (int)(threadIdx.x & 31) >= vecs) break;  // the whole warp
+      uint32_t code[2];
+      bool odd;
+      block_codes(v[i], v[i + P - 1], code[0], code[P - 1], &odd);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int c = c0 + 32 * (i + k);
+        if (c >= vecs) continue;
+        float2 x[4];
+        unpack_bf16(v[i + k], x);
+        X8[r * vecs + c] = to_e4m3(x, code[k], odd);
+        if ((c & 3) == 0) scale[r * codes + (c >> 2)] = (uint8_t)code[k];
+      }
     }
   }
 }
 
-__global__ void __launch_bounds__(THREADS) unpack8_kernel(const uint2* X8, const uint8_t* scale,
-                                                          uint4* X, int64_t rows, int32_t vecs,
-                                                          const int32_t* used, int32_t zero_tail,
-                                                          int32_t* status) {
-  const int64_t r = blockIdx.x;
-  const bool in = r < rows_in_use(used, rows, status, r == 0 && threadIdx.x == 0);
-  if (!in && !zero_tail) return;
+template <int W, int U>
+__global__ void __launch_bounds__(THREADS, BLOCKS) unpack8_kernel(
+    const uint2* X8, const uint8_t* scale, uint4* X, int64_t rows, int32_t vecs,
+    const int32_t* used, int32_t zero_tail, int32_t* status) {
+  const int64_t n = rows_in_use(used, rows, status, blockIdx.x == 0 && threadIdx.x == 0);
+  const int64_t r = my_item<W>();
+  if (r >= rows) return;
   const int64_t codes = (vecs + 3) / 4;
-  for (int c = threadIdx.x; c < vecs; c += THREADS) {
-    float x[8] = {};
-    if (in) from_e4m3(X8[r * vecs + c], code_scale(scale[r * codes + (c >> 2)]), x);
-    X[r * vecs + c] = pack_bf16(x);
+  for (int c0 = first_vec<W, U>(); c0 < vecs; c0 += W * U * 32) {
+    uint2 q[U];
+    uint8_t s[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i;
+      if (c >= vecs) continue;
+      q[i] = __ldcs(X8 + r * vecs + c);
+      s[i] = scale[r * codes + (c >> 2)];
+    }
+    if (r >= n && !zero_tail) return;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i;
+      if (c >= vecs) continue;
+      float2 x[4] = {};
+      if (r < n) from_e4m3(q[i], code_scale(s[i]), x);
+      X[r * vecs + c] = pack_bf16(x);
+    }
   }
+}
+
+// All warps of a block share a row where there are few of them (more than one piece each, or
+// there is nothing to share): a warp a row would leave most of the GPU idle. us a call in a
+// graph, shared and not, forward: 8 x 1536 2.0 and 3.3, 8 x 16384 3.9 and 18.3, 1001 x 4096 4.2
+// and 6.2; 2048 x 1536 5.5 and 4.2.
+bool share_row(int64_t items, int64_t vecs, int sms) {
+  return vecs > 32 && items <= 8 * (int64_t)sms;
 }
 
 // Sizes and indices common to both directions of SiLU-and-mul.
@@ -234,8 +364,16 @@ Params params(int64_t rows, int64_t N, const int32_t* row_of, const float* weigh
   return p;
 }
 
-unsigned grid_of(const Params& p) {
-  return (unsigned)(p.n + (p.row_of != nullptr && p.zero_tail ? p.rows : 0));
+// Blocks of the launch: for the items, and for the tail where no item stands for its rows.
+unsigned blocks_for(Params* p, bool share, int sms) {
+  const int64_t per = share ? 1 : WARPS;  // items a block
+  p->tail0 = (p->n + per - 1) / per;
+  int64_t tail = 0;
+  if (p->zero_tail && p->rows > 0) {
+    tail = (p->rows + WARPS - 1) / WARPS;
+    if (tail > 4 * sms) tail = 4 * sms;
+  }
+  return (unsigned)(p->tail0 + tail);
 }
 
 gg_status check_rows8(const void* X, const void* X8, const void* scale, int64_t rows,
@@ -272,8 +410,13 @@ gg_status gg_silu_mul(const void* H, int64_t rows, int64_t N, const int32_t* row
   p.act = static_cast<uint4*>(act);
   p.H8_out = static_cast<uint2*>(H8);
   p.scale_out = static_cast<uint8_t*>(H8_scale);
-  if (grid_of(p) == 0) return GG_OK;
-  silu_mul_kernel<<<grid_of(p), THREADS, 0, stream>>>(p);
+  const bool share = share_row(p.n, p.half / 8, sms);
+  const unsigned grid = blocks_for(&p, share, sms);
+  if (grid == 0) return GG_OK;
+  if (share && H8 != nullptr) silu_mul_kernel<WARPS, 1, true><<<grid, THREADS, 0, stream>>>(p);
+  else if (share) silu_mul_kernel<WARPS, 1, false><<<grid, THREADS, 0, stream>>>(p);
+  else if (H8 != nullptr) silu_mul_kernel<1, MANY, true><<<grid, THREADS, 0, stream>>>(p);
+  else silu_mul_kernel<1, MANY, false><<<grid, THREADS, 0, stream>>>(p);
   return launched("gg_silu_mul");
 }
 
@@ -303,8 +446,15 @@ gg_status gg_silu_mul_backward(const void* dact, const void* H, const void* H8,
   p.dH = static_cast<uint4*>(dH);
   p.act = static_cast<uint4*>(act);
   p.dweights = dweights;
-  if (grid_of(p) == 0) return GG_OK;
-  silu_mul_backward_kernel<<<grid_of(p), THREADS, 0, stream>>>(p);
+  const bool share = share_row(p.n, p.half / 8, sms);
+  const unsigned grid = blocks_for(&p, share, sms);
+  if (grid == 0) return GG_OK;
+  if (share && H8 != nullptr)
+    silu_mul_backward_kernel<WARPS, 1, true><<<grid, THREADS, 0, stream>>>(p);
+  else if (share) silu_mul_backward_kernel<WARPS, 1, false><<<grid, THREADS, 0, stream>>>(p);
+  else if (H8 != nullptr)
+    silu_mul_backward_kernel<1, MANY_BACKWARD, true><<<grid, THREADS, 0, stream>>>(p);
+  else silu_mul_backward_kernel<1, MANY_BACKWARD, false><<<grid, THREADS, 0, stream>>>(p);
   return launched("gg_silu_mul_backward");
 }
 
@@ -316,7 +466,10 @@ gg_status gg_pack8(const void* X, int64_t rows, int64_t cols, const int32_t* row
   int sms = 0;
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (rows == 0) return GG_OK;
-  pack8_kernel<<<(unsigned)rows, THREADS, 0, stream>>>(
+  const bool share = share_row(rows, cols / 8, sms);
+  const int64_t per = share ? 1 : WARPS;
+  const unsigned grid = (unsigned)((rows + per - 1) / per);
+  (share ? pack8_kernel<WARPS, 1> : pack8_kernel<1, MANY>)<<<grid, THREADS, 0, stream>>>(
       static_cast<const uint4*>(X), static_cast<uint2*>(X8), static_cast<uint8_t*>(scale), rows,
       (int32_t)(cols / 8), rows_used, dev_status);
   return launched("gg_pack8");
@@ -333,7 +486,10 @@ gg_status gg_unpack8(const void* X8, const void* scale, int64_t rows, int64_t co
   int sms = 0;
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (rows == 0) return GG_OK;
-  unpack8_kernel<<<(unsigned)rows, THREADS, 0, stream>>>(
+  const bool share = share_row(rows, cols / 8, sms);
+  const int64_t per = share ? 1 : WARPS;
+  const unsigned grid = (unsigned)((rows + per - 1) / per);
+  (share ? unpack8_kernel<WARPS, 1> : unpack8_kernel<1, MANY>)<<<grid, THREADS, 0, stream>>>(
       static_cast<const uint2*>(X8), static_cast<const uint8_t*>(scale), static_cast<uint4*>(X),
       rows, (int32_t)(cols / 8), rows_used, flags & GG_FLAG_ZERO_TAIL, dev_status);
   return launched("gg_unpack8");

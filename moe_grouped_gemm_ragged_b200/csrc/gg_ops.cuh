@@ -62,76 +62,103 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The same as pairs, which the two-wide fp32 instructions take.
+__device__ __forceinline__ void unpack_bf16(const uint4& v, float2 (&x)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float2 (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // ---- the 8-bit row form: e4m3 values under one power-of-two scale 2^(c - 127) for 32
 // columns, c the least code in [kMinCode, kMaxCode] with amax <= 448 * 2^(c - 127). With a
 // power of two the division is exact, so the only rounding is e4m3's own, to nearest even.
 // kMinCode keeps every stored value a multiple of bf16's smallest one (2^-133): restoring is
-// exact.
+// exact. What bounds these kernels next to the bytes are instructions, so the largest
+// magnitudes are found on pairs of bf16 bits, for two blocks at once.
 constexpr int kBlock = 32;
 constexpr int kMinCode = 9, kMaxCode = 247;
-
-// Code of a block whose largest finite magnitude has the fp32 bits `amax` (a value of
-// 1.m * 2^(x - 127) is above 448 * 2^(x - 135) = 1.75 * 2^(x - 127) when m is above 0.75).
-__device__ __forceinline__ uint32_t block_code(uint32_t amax) {
-  const int c = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return (uint32_t)min(max(c, kMinCode), kMaxCode);
-}
 
 __device__ __forceinline__ float code_scale(uint32_t c) { return __uint_as_float(c << 23); }
 __device__ __forceinline__ float code_inverse(uint32_t c) {
   return __uint_as_float((254u - c) << 23);
 }
 
-// Bits of the largest finite |x| of eight values (0 when there is none).
-__device__ __forceinline__ uint32_t amax_bits(const float (&x)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
-    m = max(m, a < 0x7f800000u ? a : 0u);
-  }
-  return m;
+// Magnitudes of the two bf16 in w, those of infinities and NaN as 0.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
+  const uint32_t m = w & 0x7fff7fffu;
+  return m & ~((((m + 0x00800080u) >> 15) & 0x00010001u) * 0xffffu);
 }
 
-// The same over the four lanes that hold a block's 32 columns.
-__device__ __forceinline__ uint32_t block_amax(uint32_t m) {
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+// Codes of two blocks: four neighbouring lanes hold the 32 columns of each, eight in `a` and
+// eight in `b`. The whole warp calls; *odd (the same for the warp): some value is not finite.
+__device__ __forceinline__ void block_codes(const uint4& a, const uint4& b, uint32_t& ca,
+                                            uint32_t& cb, bool* odd) {
+  constexpr uint32_t M = 0x7fff7fffu;
+  const auto over_block = [](uint32_t ma, uint32_t mb) {
+    // the halves of ma against one another in the low half, those of mb in the high half
+    uint32_t m = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  };
+  uint32_t m = over_block(__vmaxu2(__vmaxu2(a.x & M, a.y & M), __vmaxu2(a.z & M, a.w & M)),
+                          __vmaxu2(__vmaxu2(b.x & M, b.y & M), __vmaxu2(b.z & M, b.w & M)));
+  *odd = __any_sync(0xffffffffu, ((m + 0x00800080u) & 0x80008000u) != 0);
+  if (*odd)
+    m = over_block(__vmaxu2(__vmaxu2(finite_bits(a.x), finite_bits(a.y)),
+                            __vmaxu2(finite_bits(a.z), finite_bits(a.w))),
+                   __vmaxu2(__vmaxu2(finite_bits(b.x), finite_bits(b.y)),
+                            __vmaxu2(finite_bits(b.z), finite_bits(b.w))));
+  // A magnitude 1.m * 2^(x - 127) is above 448 * 2^(x - 135) = 1.75 * 2^(x - 127) when its seven
+  // bits m are above 0x60: adding 0x1f then carries into x.
+  m += 0x001f001fu;
+  ca = (uint32_t)min(max((int)((m & 0xffffu) >> 7) - 8, kMinCode), kMaxCode);
+  cb = (uint32_t)min(max((int)(m >> 23) - 8, kMinCode), kMaxCode);
 }
 
-// x over the code's scale as e4m3; an infinity becomes NaN (x * 0 + ...), which the restored
-// value shows. Under the largest code 256 would be restored as 2^128: values end at 240 there.
-__device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], uint32_t code) {
-  const float inv = code_inverse(code);
-  float v[8];
+// x over the code's scale as e4m3. Where a value is not finite (odd) infinities become NaN (x *
+// 0 + ...), which the restored value shows; under the largest code 256 would be restored as
+// 2^128, so values end at 240 there.
+__device__ __forceinline__ uint2 to_e4m3(const float2 (&x)[4], uint32_t code, bool odd) {
+  const float2 inv = both(code_inverse(code));
+  float2 v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = x[i] * inv;
-  if (code == kMaxCode) {
+  for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(x[i], inv);
+  if (odd || code == kMaxCode) {
+    const float top = code == kMaxCode ? 240.f : 448.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -240.f), 240.f);
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = __fmaf_rn(x[i].x, 0.f, fminf(fmaxf(v[i].x, -top), top));
+      v[i].y = __fmaf_rn(x[i].y, 0.f, fminf(fmaxf(v[i].y, -top), top));
+    }
   }
-  uint32_t h[4];
+  uint16_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = __fmaf_rn(x[2 * i], 0.f, v[2 * i]);
-    const float b = __fmaf_rn(x[2 * i + 1], 0.f, v[2 * i + 1]);
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    h[i] = r;
-  }
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(v[i].y), "f"(v[i].x));
+  return make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
 }
 
-__device__ __forceinline__ void from_e4m3(const uint2& q, float scale, float (&x)[8]) {
+__device__ __forceinline__ void from_e4m3(const uint2& q, float scale, float2 (&x)[4]) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint16_t pair = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(pair));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    x[2 * i] = f.x * scale;
-    x[2 * i + 1] = f.y * scale;
+    x[i] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h)), both(scale));
   }
 }
 
