@@ -138,6 +138,9 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
 __device__ __forceinline__ uint64_t key_of(double v) {
   const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
   return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
@@ -156,103 +159,37 @@ __device__ __forceinline__ float logit_or_mask(float x, bool* bad) {
 // sigma(x) e^-m for m <= 0: e^(min(x, 0) - m) / (1 + e^-|x|), which stays a normal number for
 // the largest of a token's scores however small it is when m is that score's min(x, 0).
 __device__ __forceinline__ float sigmoid_over(float x, float m) {
-  return expf(fminf(x, 0.f) - m) / (1.f + expf(-fabsf(x)));
+  return __fdividef(expf(fminf(x, 0.f) - m), 1.f + expf(-fabsf(x)));
 }
 
 // The score that a biased choice tries first. In units of 2^-23 it is off by at most
 // sigma (1 - sigma) (2 + 1.17 |x|) < 0.6 from the fast exponential, 2.5 from the sum and the
-// quotient and (1 + |bias|) / 2 from the last sum; two scores further apart than CLOSE
-// (1 + |bias| + |bias'|) are in the right order, with half of CLOSE to spare.
+// reciprocal and (1 + |bias|) / 2 from the last sum; two scores further apart than CLOSE
+// (1 + |bias| + |bias'|) are in the right order, with half of CLOSE to spare. (3 in place
+// of 1 where one of the two biases is not known.)
 __device__ __forceinline__ float fast_score(float x, float b) {
-  return __fdividef(1.f, 1.f + __expf(-x)) + b;
+  float t = x * -1.44269504f;  // 1 / (1 + 2^(-x log2 e))
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t));
+  t += 1.f;
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t));
+  return t + b;
 }
 constexpr float CLOSE = 16.f / 8388608.f;
 
+// The order is looked up this many places further than needed, to see that no other expert may
+// belong to the chosen.
+constexpr int MORE = 2;
+
+template <int SLOTS>
 struct Chosen {  // of one token, in shared memory
-  int32_t id[GG_GATE_MAX_K + 1];
-  float x[GG_GATE_MAX_K + 1];
-  float score[GG_GATE_MAX_K + 1];
+  int32_t id[SLOTS];
+  float x[SLOTS];
+  float score[SLOTS];
 };
 
-// The `want` largest keys of the group, in order, ties to the lowest expert (the lowest lane,
-// and there the lowest place, as lanes hold neighbouring experts). Returns how many there are.
-template <int G, int NV>
-__device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_t (&key)[NV],
-                                      const float (&x)[NV], Chosen& c) {
-  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
-  for (int s = 0; s < want; ++s) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) best = max(best, key[j]);
-    const uint32_t top = group_max<G>(mask, best);
-    if (top == 0) return s;  // nothing left
-    const uint32_t holders = __ballot_sync(mask, best == top);
-    if (best == top && (holders & below) == 0) {
-      bool found = false;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (!found && key[j] == top) {
-          found = true;
-          key[j] = 0;
-          c.id[s] = lane * NV + j;
-          c.x[s] = x[j];
-        }
-      }
-    }
-  }
-  return want;
-}
-
-// The same by double scores, for the few tokens whose fp32 scores do not decide: a function of
-// its own with the keys in local memory, so that it costs the others no registers.
-template <typename L, int G, int NV>
-__device__ __noinline__ int choose_double(uint32_t mask, int lane, int want, const L* row,
-                                          const float* bias, int E, Chosen* c) {
-  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
-  uint64_t key[NV];
-#pragma unroll 1
-  for (int j = 0; j < NV; ++j) {
-    const int e = lane * NV + j;
-    key[j] = 0;
-    if (e >= E) continue;
-    bool ignored = false;
-    const float x = logit_or_mask(to_float(row[e]), &ignored);
-    const float b = logit_or_mask(bias[e], &ignored);
-    if (x > -INFINITY && b > -INFINITY) key[j] = key_of(1.0 / (1.0 + exp(-(double)x)) + (double)b);
-  }
-  for (int s = 0; s < want; ++s) {
-    uint64_t best = 0;
-    int at = 0;
-#pragma unroll 1
-    for (int j = 0; j < NV; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = j;
-      }
-    const uint64_t top = group_max<G>(mask, best);
-    if (top == 0) return s;
-    const uint32_t holders = __ballot_sync(mask, best == top);
-    if (best == top && (holders & below) == 0) {
-      key[at] = 0;
-      c->id[s] = lane * NV + at;
-      c->x[s] = to_float(row[lane * NV + at]);
-    }
-  }
-  return want;
-}
-
-// bf16 logits: value and expert fit one 32-bit key, 16 bits that grow with the value over the
-// complement of the expert's number, so that the largest key names its expert and ties resolve
-// by themselves. Each lane sorts its keys once; a round compares only the lanes' first keys and
-// moves the winner's up. NaN and +inf have the largest keys (or the smallest), so the first and
-// the last of the sorted show whether a lane has any. x: the logits in fp32.
-constexpr uint32_t KEY_INF = 0xff800000u;     // of +inf
-constexpr uint32_t KEY_LOWEST = 0x00800000u;  // of the lowest finite number
-constexpr uint32_t KEY_MASKED = 0x007f0000u;  // of -inf; a NaN with its sign set is below
-
+// Batcher's odd-even merge sort of a lane's keys, largest first.
 template <int NV>
 __device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
-  // Batcher's odd-even merge sort, largest first
 #pragma unroll
   for (int p = 1; p < NV; p *= 2)
 #pragma unroll
@@ -268,11 +205,125 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
           }
 }
 
-template <int G, int NV>
-__device__ __forceinline__ int choose_bf16(uint32_t mask, int lane, int want,
-                                           const __nv_bfloat16* row, int E, bool wide,
-                                           float (&x)[NV], Chosen& c, bool* bad) {
-  const int first = lane * NV;
+// A 32-bit key: the upper 22 bits of a value's unsigned order over the complement of the
+// expert's number, so that keys differ, the largest names its expert, and of equal values the
+// lowest expert's is the largest. That is the whole of a bf16 value; fp32 values that share
+// their 22 bits may come in the wrong order. Keys below LOWEST cannot be chosen.
+constexpr uint32_t NUMBER = 0x3ffu;
+constexpr uint32_t LOWEST = 0x00800000u;  // of the lowest finite number
+static_assert(GG_MAX_EXPERTS <= NUMBER + 1, "an expert's number fits the key");
+__device__ __forceinline__ uint32_t packed(float v, int expert) {
+  return (key_of(v) & ~NUMBER) | (NUMBER - expert);
+}
+__device__ __forceinline__ int expert_of(uint32_t key) { return (int)(NUMBER - (key & NUMBER)); }
+
+// The `want` largest keys of the group, in order, into c.id. Each lane sorts its keys once; a
+// round compares only the lanes' first keys and moves the winner's up. Returns how many there
+// are.
+template <int G, int NV, typename C>
+__device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_t (&key)[NV],
+                                      C& c) {
+  for (int s = 0; s < want; ++s) {
+    const uint32_t top = group_max<G>(mask, key[0]);
+    if (top < LOWEST) return s;  // nothing left
+    const bool won = key[0] == top;
+#pragma unroll
+    for (int j = 0; j + 1 < NV; ++j) key[j] = won ? key[j + 1] : key[j];
+    key[NV - 1] = won ? 0u : key[NV - 1];
+    if (lane == 0) c.id[s] = (int32_t)top;
+  }
+  return want;
+}
+
+// What decides the order: sigma(x) + b under a bias, else x.
+template <bool BIAS>
+__device__ __forceinline__ double double_score(float x, float b) {
+  return BIAS ? 1.0 / (1.0 + exp(-(double)x)) + (double)b : (double)x;
+}
+
+// Orders n candidates by their doubles, ties to the lowest expert: each finds its place.
+template <int G, bool BIAS, typename C>
+__device__ __forceinline__ void order_double(uint32_t mask, int lane, int n, const float* bias,
+                                             C& c, double* d) {
+#pragma unroll 1
+  for (int s = lane; s < n; s += G)
+    d[s] = double_score<BIAS>(c.x[s], BIAS ? bias[c.id[s]] : 0.f);
+  __syncwarp(mask);
+  constexpr int PER = (GG_GATE_MAX_K + MORE + G - 1) / G;
+  int32_t id[PER], place[PER];
+  float x[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int s = lane + i * G;
+    if (s >= n) continue;
+    id[i] = c.id[s];
+    x[i] = c.x[s];
+    place[i] = 0;
+#pragma unroll 1
+    for (int q = 0; q < n; ++q)
+      place[i] += d[q] > d[s] || (d[q] == d[s] && c.id[q] < id[i]);
+  }
+  __syncwarp(mask);
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (lane + i * G < n) {
+      c.id[place[i]] = id[i];
+      c.x[place[i]] = x[i];
+    }
+}
+
+// All of the token's experts by doubles, for the very few tokens that need it: a function of its
+// own with the keys in local memory, so that it costs the others no registers.
+template <typename L, int G, int NV, bool BIAS>
+__device__ __noinline__ int choose_double(uint32_t mask, int lane, int want, const L* row,
+                                          const float* bias, int E, int32_t* ids) {
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+  uint64_t key[NV];
+#pragma unroll 1
+  for (int j = 0; j < NV; ++j) {
+    const int e = lane * NV + j;
+    key[j] = 0;
+    if (e >= E) continue;
+    bool ignored = false;
+    const float x = logit_or_mask(to_float(row[e]), &ignored);
+    if constexpr (BIAS) {
+      const float b = logit_or_mask(bias[e], &ignored);
+      if (x > -INFINITY && b > -INFINITY)
+        key[j] = key_of(double_score<BIAS>(x, b));
+    } else {
+      if (x > -INFINITY) key[j] = key_of(double_score<BIAS>(x, 0.f));
+    }
+  }
+  for (int s = 0; s < want; ++s) {
+    uint64_t best = 0;
+    int at = 0;
+#pragma unroll 1
+    for (int j = 0; j < NV; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+      }
+    const uint64_t top = group_max<G>(mask, best);
+    if (top == 0) return s;
+    const uint32_t holders = __ballot_sync(mask, best == top);
+    if (best == top && (holders & below) == 0) {
+      key[at] = 0;
+      ids[s] = lane * NV + at;
+    }
+  }
+  return want;
+}
+
+// Sorted keys of a lane's bf16 logits, made two at a time, and the logits in fp32. NaN and +inf
+// have the largest keys (with their sign set the smallest), so the first and the last of the
+// sorted show whether a lane has any.
+constexpr uint32_t KEY_INF = 0xff800000u;     // of +inf
+constexpr uint32_t KEY_MASKED = 0x007f0000u;  // of -inf
+
+template <int NV>
+__device__ __forceinline__ void bf16_keys(uint32_t mask, int first, const __nv_bfloat16* row,
+                                          int E, bool wide, uint32_t (&key)[NV], float (&x)[NV],
+                                          bool* bad) {
   uint32_t w[NV / 2];  // two logits each
 #pragma unroll
   for (int j = 0; j < NV / 2; j += 4) {
@@ -288,7 +339,6 @@ __device__ __forceinline__ int choose_bf16(uint32_t mask, int lane, int want,
       }
     }
   }
-  uint32_t key[NV];
   const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NV / 2; ++i) {
@@ -297,7 +347,7 @@ __device__ __forceinline__ int choose_bf16(uint32_t mask, int lane, int want,
     const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), zero);
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
     const uint32_t k = u ^ (((u >> 15) & 0x00010001u) * 0xffffu | 0x80008000u);
-    const uint32_t number = GG_MAX_EXPERTS - 1 - (first + 2 * i);
+    const uint32_t number = NUMBER - (first + 2 * i);
     key[2 * i] = (k << 16) | number;
     key[2 * i + 1] = (k & 0xffff0000u) | (number - 1);
     x[2 * i] = __uint_as_float(w[i] << 16);
@@ -314,20 +364,6 @@ __device__ __forceinline__ int choose_bf16(uint32_t mask, int lane, int want,
       x[j] = logit_or_mask(x[j], bad);
     }
   }
-  for (int s = 0; s < want; ++s) {
-    const uint32_t top = group_max<G>(mask, key[0]);
-    if (top < KEY_LOWEST) return s;  // only masked ones left
-    const bool won = key[0] == top;  // one lane: the keys differ
-#pragma unroll
-    for (int j = 0; j + 1 < NV; ++j) key[j] = won ? key[j + 1] : key[j];
-    key[NV - 1] = won ? 0u : key[NV - 1];
-    if (won) {
-      const uint32_t v = top & 0xffff0000u;
-      c.id[s] = GG_MAX_EXPERTS - 1 - (int)(top & 0xffffu);
-      c.x[s] = __uint_as_float((v >> 31) ? v ^ 0x80000000u : v ^ 0xffff0000u);
-    }
-  }
-  return want;
 }
 
 template <int G>
@@ -337,19 +373,23 @@ __device__ __forceinline__ uint32_t group_mask() {
 
 // Choice by the logit itself without a bias (both scores grow with it, so the choice is
 // exact), by sigma(x) + bias in double precision with one: neighbours of 256 scores are often
-// closer than fp32 tells apart. With a bias fp32 scores come first, one place further than
-// needed: only a token with two neighbours in that order within CLOSE of one another (other
-// than the same logit under the same bias, a tie in any precision; at the last place any two,
-// as others may lie behind them) is chosen again in double precision.
+// closer than fp32 tells apart. fp32 logits and fp32 scores are looked up MORE places further
+// than needed, which leaves three cases: each two neighbours are in order for sure (values apart,
+// or equal logits under equal biases, a tie in any precision); some are not, but nothing behind
+// the last one can belong to the first k: those looked up are put in order by doubles; or the
+// k-th and the last are too close for that: all experts are looked through again by doubles.
 template <typename L, int G, int NV, bool BIAS>
 __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, bool renorm,
                                                        bool wide, bool wide_bias) {
-  __shared__ Chosen chosen[THREADS / G];
+  constexpr bool EXACT = !BIAS && sizeof(L) == 2;  // the keys hold the whole value
+  constexpr int SLOTS = GG_GATE_MAX_K + (EXACT ? 0 : MORE);
+  __shared__ Chosen<SLOTS> chosen[THREADS / G];
+  __shared__ double doubles[EXACT ? 1 : THREADS / G][EXACT ? 1 : SLOTS];
   const int lane = threadIdx.x % G;
   const int64_t t = (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G;
   if (t >= p.T) return;  // the whole group
   const uint32_t mask = group_mask<G>();
-  Chosen& c = chosen[threadIdx.x / G];
+  Chosen<SLOTS>& c = chosen[threadIdx.x / G];
   const L* row = static_cast<const L*>(p.logits) + t * p.E;
   bool bad_count = false, bad = false;
   int64_t live_tokens = p.T;
@@ -360,74 +400,114 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
   float x[NV];
   int got = 0;
   if (t < live_tokens) {
-    if constexpr (!BIAS && sizeof(L) == 2) {
-      got = choose_bf16<G, NV>(mask, lane, p.k, row, p.E, wide, x, c, &bad);
+    uint32_t key[NV];
+    const int want = EXACT ? p.k : min(p.k + MORE, p.E);
+    if constexpr (EXACT) {
+      bf16_keys<NV>(mask, lane * NV, row, p.E, wide, key, x, &bad);
     } else {
       load_row<NV>(row, lane * NV, p.E, wide, x);
+      float b[NV];
+      if constexpr (BIAS) load_row<NV>(p.bias, lane * NV, p.E, wide_bias, b);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) x[j] = logit_or_mask(x[j], &bad);
-      uint32_t key[NV];
-      if constexpr (BIAS) {
-        float b[NV];
-        load_row<NV>(p.bias, lane * NV, p.E, wide_bias, b);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          if (x[j] > -INFINITY) b[j] = logit_or_mask(b[j], &bad);
-          const bool in = x[j] > -INFINITY && b[j] > -INFINITY;
-          key[j] = in ? key_of(fast_score(x[j], b[j])) : 0u;
+      for (int j = 0; j < NV; ++j) {
+        bool in = fabsf(x[j]) < INFINITY;
+        bad |= !(x[j] < INFINITY);
+        if constexpr (BIAS) {
+          bad |= in && !(b[j] < INFINITY);
+          in = in && fabsf(b[j]) < INFINITY;
+          key[j] = in ? packed(fast_score(x[j], b[j]), lane * NV + j) : 0u;
+        } else {
+          key[j] = in ? packed(x[j], lane * NV + j) : 0u;
+          x[j] = in ? x[j] : -INFINITY;
         }
-        got = choose<G, NV>(mask, lane, min(p.k + 1, p.E), key, x, c);
-        __syncwarp(mask);
-        bool undecided = false;
-        for (int s = lane; s + 1 < got; s += G) {
-          const float xa = c.x[s], xb = c.x[s + 1];
-          const float ba = p.bias[c.id[s]], bb = p.bias[c.id[s + 1]];
-          const float gap = fast_score(xa, ba) - fast_score(xb, bb);
-          undecided |= gap <= CLOSE * (1.f + fabsf(ba) + fabsf(bb)) &&
-                       (s + 1 == p.k || !(xa == xb && ba == bb));
-        }
-        if (__any_sync(mask, undecided))
-          got = choose_double<L, G, NV>(mask, lane, p.k, row, p.bias, p.E, &c);
-        got = min(got, p.k);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) key[j] = x[j] > -INFINITY ? key_of(x[j]) : 0u;
-        got = choose<G, NV>(mask, lane, p.k, key, x, c);
       }
+      sort_keys(key);
+    }
+    got = choose<G, NV>(mask, lane, want, key, c);
+    __syncwarp(mask);
+#pragma unroll 1
+    for (int s = lane; s < got; s += G) {
+      const uint32_t k = (uint32_t)c.id[s];
+      const int id = expert_of(k);
+      c.id[s] = id;
+      if constexpr (EXACT)  // the key's value again
+        c.x[s] = value_of((k & 0xffff0000u) | ((k >> 31) ? 0u : 0xffffu));
+      else c.x[s] = to_float(row[id]);
+      if constexpr (BIAS) c.score[s] = fast_score(c.x[s], p.bias[id]);
+    }
+    if constexpr (!EXACT) {
+      __syncwarp(mask);
+      bool close = false, open = false;
+#pragma unroll 1
+      for (int s = lane; s < got; s += G) {
+        const bool kth = s == p.k - 1 && got == want && want < p.E;
+        if constexpr (BIAS) {
+          const float ba = p.bias[c.id[s]];
+          if (s + 1 < got) {
+            const float bb = p.bias[c.id[s + 1]];
+            close |= c.score[s] - c.score[s + 1] <= CLOSE * (1.f + fabsf(ba) + fabsf(bb)) &&
+                     !(c.x[s] == c.x[s + 1] && ba == bb);
+          }
+          if (kth) {
+            const float bb = p.bias[c.id[got - 1]];
+            // the first k are at least at the k-th's 22 bits, what follows at most at the last's
+            open = value_of(key_of(c.score[s]) & ~NUMBER) -
+                       value_of(key_of(c.score[got - 1]) | NUMBER) <=
+                   CLOSE * (3.f + fabsf(ba) + fabsf(bb));
+          }
+        } else {
+          const float x0 = c.x[s];
+          if (s + 1 < got) {
+            const float x1 = c.x[s + 1];
+            close |= !(x0 > x1 || (x0 == x1 && c.id[s] < c.id[s + 1]));
+          }
+          if (kth) open = (key_of(x0) ^ key_of(c.x[got - 1])) <= NUMBER;
+        }
+      }
+      if (__any_sync(mask, open)) {
+        got = choose_double<L, G, NV, BIAS>(mask, lane, p.k, row, p.bias, p.E, c.id);
+        __syncwarp(mask);
+        for (int s = lane; s < got; s += G) c.x[s] = to_float(row[c.id[s]]);
+      } else if (__any_sync(mask, close)) {
+        order_double<G, BIAS>(mask, lane, got, p.bias, c, doubles[threadIdx.x / G]);
+      }
+      got = min(got, p.k);
     }
     __syncwarp(mask);
   }
-  float m = 0.f, total = 1.f;
+  float m = 0.f, inv = 1.f;
   if (got > 0 && (renorm || !sigmoid)) {
     // shares: each score over the sum of the chosen (renorm) or of all (softmax), both relative
-    // to the largest
-    m = sigmoid ? -INFINITY : c.x[0];
-    if (sigmoid) {
-      for (int s = lane; s < got; s += G) m = fmaxf(m, fminf(c.x[s], 0.f));
+    // to the largest; without a bias the first has it
+    m = c.x[0];
+    if constexpr (BIAS) {
+      m = -INFINITY;
+#pragma unroll 1
+      for (int s = lane; s < got; s += G) m = fmaxf(m, c.x[s]);
       m = group_max<G>(mask, m);
     }
-    total = 0.f;
-    if constexpr (!BIAS) {  // a biased gate is a sigmoid
-      if (!renorm) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) total += expf(x[j] - m);  // 0 of -inf
-      }
-    }
+    if (sigmoid) m = fminf(m, 0.f);
+    float total = 0.f;
     if (renorm) {
+#pragma unroll 1
       for (int s = lane; s < got; s += G) {
         const float v = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
         c.score[s] = v;
         total += v;
       }
+    } else if constexpr (!BIAS) {  // a biased gate is a sigmoid
+#pragma unroll
+      for (int j = 0; j < NV; ++j) total += expf(x[j] - m);  // 0 of -inf
     }
-    total = group_sum<G>(mask, total);
+    inv = __fdividef(1.f, group_sum<G>(mask, total));
   }
+#pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
     float w = 0.f;
     if (s < got) {
       if (renorm) w = c.score[s];
       else w = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
-      w = p.scale * __fdividef(w, total);
+      w *= p.scale * inv;
     }
     p.ids[t * p.k + s] = s < got ? c.id[s] : -1;
     p.weights[t * p.k + s] = w;
@@ -444,11 +524,12 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 // The scores are computed again from the logits; dx of a logit that was not chosen is 0 but for
 // the first form. A slot of id -1 carries nothing. A row in shared memory brings the slots to
 // their experts' lanes: it takes g (first form) or dx (the others), slot after slot, so that
-// slots of the same expert add up in their order.
+// slots of the same expert add up in their order (finding equal slots first and adding the others
+// at once took longer: 9.5 us against 8.3 for 32768 x 64 top 8).
 template <typename L, int G, int NV>
 __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool sigmoid,
                                                                 bool renorm, bool wide) {
-  __shared__ Chosen chosen[THREADS / G];
+  __shared__ Chosen<GG_GATE_MAX_K> chosen[THREADS / G];
   // four experts of every lane side by side, then the next four: lanes' vectors are neighbours;
   // 16 floats more put the rows of two 4-lane groups into different banks
   __shared__ __align__(16) float rows[THREADS / G][G * NV + 16];
@@ -456,7 +537,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
   const int64_t t = (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G;
   if (t >= p.T) return;  // the whole group
   const uint32_t mask = group_mask<G>();
-  Chosen& c = chosen[threadIdx.x / G];  // each lane reads only its own slots
+  auto& c = chosen[threadIdx.x / G];  // each lane reads only its own slots
   float* d = rows[threadIdx.x / G];
   const L* row = static_cast<const L*>(p.logits) + t * p.E;
   const bool full = !sigmoid && !renorm;
@@ -553,7 +634,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
 template <int N> using Int = std::integral_constant<int, N>;
 
 // Lanes a token and experts a lane. A warp for each token is the quickest for few of them, NV
-// experts a lane and so more tokens a warp the cheapest in instructions for many.
+// experts a lane and so several tokens a warp the cheapest in instructions for many.
 template <int NV, typename F>
 void by_experts(int E, bool few, const F& f) {
   if (few && E <= 64) f(Int<32>(), Int<2>());
@@ -566,17 +647,17 @@ void by_experts(int E, bool few, const F& f) {
   else f(Int<32>(), Int<32>());
 }
 
-// 1 x 64 bf16: 2.4 us a call in a graph with a warp a token, 3.3 us with four lanes; 32768 x
-// 64: 16.2 and 7.7 us. The two break even where the warps fill the GPU (148 SMs x 32 or so).
+// 1 x 64 bf16: 2.2 us a call in a graph with a warp a token, 3.3 us with four lanes; 32768 x
+// 64: 16.2 and 7.3 us. The two break even where the warps fill the GPU (148 SMs x 32 or so).
 constexpr int64_t FEW = 4096;
 
 template <typename L, bool BIAS>
 void launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16);
   const bool wide_bias = p.E % 8 == 0 && !misaligned(p.bias, 16);
-  // sorted keys take sixteen experts a lane well (8: 8.8 us for 32768 x 64), the fp32 search,
-  // which looks through a lane's keys in each round, eight (16411 x 256 with a bias: 22.6 us,
-  // 28.1 with sixteen)
+  // sixteen experts a lane and so more tokens a warp for bf16 (7.3 us for 32768 x 64, 8.3 with
+  // eight), eight for fp32, whose looking-up further and checking is shared by few tokens anyway
+  // (16411 x 256 with a bias: 16.5 us, 19.1 with sixteen)
   constexpr int MANY = !BIAS && sizeof(L) == 2 ? 16 : 8;
   by_experts<MANY>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
