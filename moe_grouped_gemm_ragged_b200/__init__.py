@@ -128,10 +128,12 @@ def testing_force_variant(variant: int) -> int:
     return int(lib().gg_testing_force_variant(int(variant)))
 
 
-def _stream_handle(stream) -> int:
+def _stream_handle(stream, device: Optional[int] = None) -> int:
+    """The stream's handle (None: the current stream of ``device``, the current one)."""
     if stream is None:
         # the handle itself: building a torch.cuda.Stream costs 3 us, a third of a small call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

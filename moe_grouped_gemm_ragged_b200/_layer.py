@@ -121,7 +121,7 @@ def gate_topk(logits: torch.Tensor, k: int, *, score: int = GATE_SOFTMAX, renorm
     rc = lib().gg_gate_topk(
         logits.data_ptr(), T, E, k, _arg(bias, "bias", (E,), _F32, dev), score, flags, scale,
         _arg(num_tokens, "num_tokens", (1,), _I32, dev), _arg(ids, "topk_ids", (T, k), _I32, dev),
-        _arg(w, "weights", (T, k), _F32, dev), _status_ptr(status), _stream_handle(stream))
+        _arg(w, "weights", (T, k), _F32, dev), _status_ptr(status), _stream_handle(stream, dev))
     _raise(rc, "gg_gate_topk")
     return ids, w
 
@@ -142,7 +142,7 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
         logits.data_ptr(), T, E, k, score, flags, scale, topk_ids.data_ptr(),
         _arg(dweights, "dweights", (T, k), _F32, dev),
         _arg(out, "dlogits", (T, E), logits.dtype, dev), _status_ptr(status),
-        _stream_handle(stream))
+        _stream_handle(stream, dev))
     _raise(rc, "gg_gate_topk_backward")
     return out
 
@@ -174,7 +174,7 @@ def unroute(Y: torch.Tensor, row_of: torch.Tensor, k: int, out: Optional[torch.T
     rc = lib().gg_unroute(Y.data_ptr(), rows, rp, _arg(weights, "weights", (T, k), _F32, dev),
                           _arg(residual, "residual", (T, N), _BF16, dev), T, k, N,
                           _arg(out, "out", (T, N), _BF16, dev), _status_ptr(status),
-                          _stream_handle(stream))
+                          _stream_handle(stream, dev))
     _raise(rc, "gg_unroute")
     return out
 
@@ -206,7 +206,7 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
         _arg(weights, "weights", (T, k), _F32, dev), T, k, N, _used_ptr(offs, zero_tail),
         FLAG_ZERO_TAIL if zero_tail else 0, _arg(dY, "dY", (rows, N), _BF16, dev),
         _arg(dweights, "dweights", (T, k), _F32, dev), _status_ptr(status),
-        _stream_handle(stream))
+        _stream_handle(stream, dev))
     _raise(rc, "gg_unroute_backward")
     return dY, dweights
 
@@ -271,7 +271,7 @@ def silu_mul(H: torch.Tensor, act: Optional[torch.Tensor] = None, *,
     act = _new(act, (rows, N // 2), _BF16, H, stream)
     rc = lib().gg_silu_mul(H.data_ptr(), rows, N, used, rp, n, wp, flags,
                            _arg(act, "act", (rows, N // 2), _BF16, dev), p8, ps,
-                           _status_ptr(status), _stream_handle(stream))
+                           _status_ptr(status), _stream_handle(stream, dev))
     _raise(rc, "gg_silu_mul")
     return act
 
@@ -303,7 +303,7 @@ def silu_mul_backward(dact: torch.Tensor, dH: Optional[torch.Tensor] = None, *,
         flags, _arg(dH, "dH", (rows, N), _BF16, dev),
         _arg(act, "act", (rows, half), _BF16, dev),
         _per_row(dweights, "dweights", rows if row_of is None else n), _status_ptr(status),
-        _stream_handle(stream))
+        _stream_handle(stream, dev))
     _raise(rc, "gg_silu_mul_backward")
     return dH
 
@@ -322,7 +322,7 @@ def pack8(X: torch.Tensor, X8: Optional[torch.Tensor] = None,
     rc = lib().gg_pack8(X.data_ptr(), rows, cols, _used_ptr(offs, False),
                         _arg(X8, "X8", (rows, cols), _E4M3, dev),
                         _arg(scale, "scale", (rows, codes), _E8M0, dev), _status_ptr(status),
-                        _stream_handle(stream))
+                        _stream_handle(stream, dev))
     _raise(rc, "gg_pack8")
     return X8, scale
 
@@ -338,7 +338,7 @@ def unpack8(X8: torch.Tensor, scale: torch.Tensor, X: Optional[torch.Tensor] = N
     rc = lib().gg_unpack8(
         X8.data_ptr(), _arg(scale, "scale", (rows, (cols + BLOCK8 - 1) // BLOCK8), _E8M0, dev),
         rows, cols, _used_ptr(offs, zero_tail), FLAG_ZERO_TAIL if zero_tail else 0,
-        _arg(X, "X", (rows, cols), _BF16, dev), _status_ptr(status), _stream_handle(stream))
+        _arg(X, "X", (rows, cols), _BF16, dev), _status_ptr(status), _stream_handle(stream, dev))
     _raise(rc, "gg_unpack8")
     return X
 

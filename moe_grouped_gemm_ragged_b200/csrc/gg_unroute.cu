@@ -233,7 +233,7 @@ gg_status gg_unroute_backward(const void* dout, const void* Y, int64_t rows,
   if (s != GG_OK) return s;
   if (flags & ~GG_FLAG_ZERO_TAIL) return GG_ERR_INVALID_ARG;
   const bool zero = (flags & GG_FLAG_ZERO_TAIL) != 0;
-  if (zero && (rows_used == nullptr || dY == nullptr)) return GG_ERR_INVALID_ARG;
+  if (zero && (rows_used == nullptr || (dY == nullptr && rows > 0))) return GG_ERR_INVALID_ARG;
   if (misaligned(Y, 16) || misaligned(dout, 16) || misaligned(dY, 16) || misaligned(row_of, 4) ||
       misaligned(weights, 4) || misaligned(dweights, 4) || misaligned(rows_used, 4))
     return GG_ERR_UNSUPPORTED;

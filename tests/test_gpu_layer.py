@@ -572,6 +572,147 @@ def test_layer_forward_and_gradients(ckpt8, where):
     assert torch.equal(grads[4].cpu(), dout)
 
 
+@pytest.mark.parametrize("ckpt8", [False, True])
+@pytest.mark.parametrize("T,used", [(0, 0), (1, 1), (5, 0), (40, 13)])
+def test_layer_of_few_and_of_unused_tokens(T, used, ckpt8):
+    """No token, one, a padded batch without any and with some: outputs and gradients of unused
+    tokens are the residual's and zeros, those of the others as if the batch were not padded."""
+    X, x, W1, W2, res, dout = (t.cuda() for t in _layer_inputs())
+    x[5], x[9] = x[6], x[7]
+    k, E = 3, 8
+
+    def layer(n, num):
+        leaves = [t.clone().requires_grad_(True) for t in (X[:n], x[:n], W1, W2, res[:n])]
+        st = _status()
+        ids, w = gg.gate(leaves[1], k, num_tokens=num, status=st)
+        A, row_of, offs = gg.dispatch(leaves[0], ids, E, status=st)
+        Y = gg.expert_mlp(A, leaves[2], leaves[3], offs, row_of=row_of, weights=w, ckpt8=ckpt8,
+                          status=st)
+        out = gg.combine(Y, row_of, k, residual=leaves[4], offs=offs, status=st)
+        grads = torch.autograd.grad(out, leaves, dout[:n])
+        assert int(st.item()) & gg.DEV_ERROR_MASK == 0
+        return out.detach(), grads
+
+    num = torch.tensor([used], dtype=torch.int32, device="cuda")
+    out, grads = layer(T, num)
+    want, wgrads = layer(used, None)
+    assert torch.equal(out[:used], want) and torch.equal(out[used:], res[used:T])
+    for i in (0, 1):
+        assert torch.equal(grads[i][:used], wgrads[i])
+        assert bool((grads[i][used:] == 0).all())
+    for i in (2, 3):
+        assert torch.equal(grads[i], wgrads[i])
+    if used == 0:
+        assert bool((grads[2] == 0).all()) and bool((grads[3] == 0).all())
+
+
+def test_expert_mlp_equals_its_parts():
+    """expert_mlp without and with weights by row, W stored [E, N, K], both column layouts, with
+    and without the 8-bit checkpoint, equals grouped_mm, swiglu and grouped_mm bit for bit."""
+    rng = np.random.default_rng(12)
+    offs = torch.tensor([0, 70, 70, 201], dtype=torch.int32, device="cuda")
+    A = _bf16(rng.normal(size=(210, 128))).cuda()
+    A[201:] = float("nan")
+    W1, W2 = _bf16(rng.normal(size=(4, 128, 512)) / 8).cuda(), _bf16(
+        rng.normal(size=(4, 256, 136)) / 8).cuda()
+    w = torch.rand(210, device="cuda")
+    dY = _bf16(rng.normal(size=(210, 136))).cuda()
+    for nk in (False, True):
+        ws = [t.transpose(1, 2).contiguous() if nk else t for t in (W1, W2)]
+        for concat in (False, True):
+            for weights in (None, w):
+                for ckpt8 in (False, True):
+                    runs = []
+                    for whole in (True, False):
+                        leaves = [t.detach().clone().requires_grad_(True)
+                                  for t in [A, *ws] + ([w] if weights is not None else [])]
+                        wt = leaves[3] if weights is not None else None
+                        if whole:
+                            Y = gg.expert_mlp(leaves[0], leaves[1], leaves[2], offs, weights=wt,
+                                              gate_up_concat=concat, w_nk=nk, ckpt8=ckpt8)
+                        else:
+                            H = gg.grouped_mm(leaves[0], leaves[1], offs, w_nk=nk, ckpt8=ckpt8)
+                            act = gg.swiglu(H, offs, weights=wt, gate_up_concat=concat,
+                                            ckpt8=ckpt8)
+                            Y = gg.grouped_mm(act, leaves[2], offs, w_nk=nk)
+                        runs.append([Y.detach(), *torch.autograd.grad(Y, leaves, dY)])
+                    for i, (a, b) in enumerate(zip(*runs)):
+                        if i == 3 and ckpt8:
+                            continue  # W2's gradient: from the activation's second computation
+                        assert torch.equal(a, b), (nk, concat, ckpt8, i)
+
+
+def test_checkpoints_in_8_bits_take_half_the_memory():
+    rows, K, N = 4096, 512, 1024
+    offs = torch.tensor([rows // 2, rows], dtype=torch.int32, device="cuda")
+    A = torch.randn(rows, K, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    W1 = torch.randn(2, K, N, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    W2 = torch.randn(2, N // 2, K, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    kept = []
+    for ckpt8 in (False, True):
+        before = torch.cuda.memory_allocated()
+        # A is the caller's to free: a copy that only the layer holds
+        Y = gg.expert_mlp(A * 1, W1, W2, offs, ckpt8=ckpt8)
+        kept.append(torch.cuda.memory_allocated() - before - Y.nbytes)
+        del Y
+    whole = 2 * rows * (K + N)
+    assert whole <= kept[0] < 1.01 * whole
+    assert kept[1] <= whole * 33 / 64 + (1 << 16)
+
+
+def test_gate_gradient_of_an_expert_named_twice():
+    """ids that gate_topk would not make: both slots add to their expert, in order."""
+    x = torch.randn(3, 40, generator=torch.Generator().manual_seed(8))
+    ids = torch.tensor([[4, 4, 4], [1, 2, 1], [39, -1, 39]], dtype=torch.int32)
+    dw = torch.randn(3, 3, generator=torch.Generator().manual_seed(9))
+    for score in (gg.GATE_SOFTMAX, gg.GATE_SIGMOID):
+        for renorm in (False, True):
+            dx = gg.gate_topk_backward(x.cuda(), ids.cuda(), dw.cuda(), score=score, renorm=renorm)
+            ref = ol.gate_backward(x.double().numpy(), ids.numpy(), dw.double().numpy(),
+                                   score == gg.GATE_SIGMOID, renorm)
+            # |dw| below 4, a few dozen roundings
+            _near(dx.cpu().double().numpy(), ref, 256 * U, "dlogits")
+            again = gg.gate_topk_backward(x.cuda(), ids.cuda(), dw.cuda(), score=score,
+                                          renorm=renorm)
+            assert torch.equal(dx, again)
+
+
+def test_captured_autograd_layer():
+    """The autograd forms captured with their backward pass (leaves without an eager graph),
+    replayed on new inputs, equal eager ones bit for bit."""
+    inputs = [t.cuda() for t in _layer_inputs()]
+    k, E = 3, 8
+
+    def layer(leaves, dout):
+        ids, w = gg.gate(leaves[1], k, score=gg.GATE_SIGMOID, scale=2.0)
+        A, row_of, offs = gg.dispatch(leaves[0], ids, E)
+        Y = gg.expert_mlp(A, leaves[2], leaves[3], offs, row_of=row_of, weights=w, ckpt8=True)
+        out = gg.combine(Y, row_of, k, residual=leaves[4], offs=offs)
+        return [out.detach(), *torch.autograd.grad(out, leaves, dout)]
+
+    static = [t.clone().requires_grad_(i < 5) for i, t in enumerate(inputs)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            layer(static[:5], static[5])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = layer(static[:5], static[5])
+    for seed in (1, 2):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        with torch.no_grad():
+            for s, t in zip(static, inputs):
+                s.copy_(t.flip(0) + 0.25 * torch.randn(t.shape, generator=gen, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got_now = [t.clone() for t in got]
+        fresh = [t.detach().clone().requires_grad_(i < 5) for i, t in enumerate(static)]
+        for a, b in zip(got_now, layer(fresh[:5], fresh[5])):
+            assert torch.equal(a, b)
+
+
 def test_swiglu_weights_and_partial_gradients():
     """Gradients asked for one by one equal those asked for together; an expanded and a
     misaligned gradient are taken."""
