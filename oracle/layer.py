@@ -40,12 +40,8 @@ def gate(x, k, sigmoid=False, renorm=True, scale=1.0, bias=None, num_tokens=None
     if bias is not None:
         b = _mask(np.asarray(bias, np.float64))
         key = np.where(np.isneginf(x) | np.isneginf(b), -np.inf, np.exp(_log_sigmoid(x)) + b)
-    ids = np.full((T, k), -1, np.int64)
-    for t in range(T):
-        order = sorted(range(E), key=lambda e: (-key[t, e], e))
-        for s in range(k):
-            if key[t, order[s]] > -np.inf:
-                ids[t, s] = order[s]
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :k]  # equal keys: the lowest expert first
+    ids = np.where(np.take_along_axis(key, ids, 1) > -np.inf, ids, -1)
     return ids, scale * _weights(x, ids, sigmoid, renorm)
 
 

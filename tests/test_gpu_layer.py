@@ -99,6 +99,21 @@ def test_gate(T, E, k, sigmoid, renorm, dtype):
         _check_gate(x, k, True, renorm, 1.0, bias=0.3 * torch.randn(E, generator=gen))
 
 
+@pytest.mark.parametrize("E,k,dtype", [(5, 5, torch.bfloat16), (33, 4, torch.float32),
+                                       (64, 8, torch.bfloat16), (64, 6, torch.float32),
+                                       (100, 3, torch.bfloat16), (128, 8, torch.float32),
+                                       (160, 8, torch.bfloat16), (256, 6, torch.float32),
+                                       (400, 2, torch.bfloat16), (1000, 32, torch.float32)])
+def test_gate_of_many_tokens(E, k, dtype):
+    """Several tokens a warp (above 4096), the last group of them short, some not in use."""
+    gen = torch.Generator().manual_seed(E)
+    x = (2 * torch.randn(4099, E, generator=gen)).to(dtype)
+    x[torch.rand(4099, E, generator=gen) < 0.2] = -float("inf")
+    _check_gate(x, k, False, E % 2 == 0, 1.5, num=4090)
+    _check_gate(x, k, True, E % 3 == 0, 1.0, num=4090,
+                bias=0.3 * torch.randn(E, generator=gen) if E % 2 == 0 else None)
+
+
 @pytest.mark.parametrize("sigmoid,renorm", [(False, False), (False, True), (True, False),
                                             (True, True)])
 def test_gate_masks_and_far_values(sigmoid, renorm):
@@ -212,7 +227,11 @@ def _routing(T, k, E, seed, dropped=0.1):
 
 @pytest.mark.parametrize("T,k,E,N", [(1, 1, 4, 8), (1, 8, 8, 2048), (3, 2, 5, 16), (37, 3, 6, 136),
                                      (130, 8, 16, 1160), (65, 10, 12, 264), (20, 33, 40, 520),
-                                     (5, 8, 64, 7168), (2, 4, 16, 8200)])
+                                     (5, 8, 64, 7168), (2, 4, 16, 8200),
+                                     # several tokens a thread (above 1184) of 1 to 9 slots
+                                     (1301, 1, 4, 72), (1303, 2, 6, 264), (1250, 3, 6, 40),
+                                     (1191, 4, 8, 1096), (1200, 5, 8, 24), (1187, 9, 12, 16),
+                                     (600, 1, 4, 2312)])
 @pytest.mark.parametrize("weighted,residual", [(False, False), (True, False), (True, True)])
 def test_unroute(T, k, E, N, weighted, residual):
     row_of, offs, n = _routing(T, k, E, seed=T + N)
@@ -325,7 +344,8 @@ def _wild_rows(R, C, seed):
 
 
 @pytest.mark.parametrize("R,C", [(1, 8), (1, 2048), (5, 32), (3, 40), (65, 136), (130, 1160),
-                                 (4, 8200), (7, 56)])
+                                 (4, 8200), (7, 56),
+                                 (1201, 264), (1190, 1160)])  # a warp a row of several pieces
 def test_rows8_bit_exact(R, C):
     x = _wild_rows(R, C, R + C)
     blocks = -(-C // 32)
@@ -390,7 +410,10 @@ FLUSHED = 2.0 ** -100
 
 @pytest.mark.parametrize("rows,N,concat", [(1, 256, False), (8, 1536, True), (37, 512, False),
                                            (5, 16, True), (9, 80, True), (33, 1040, True),
-                                           (3, 4096, False), (2, 16400, True)])
+                                           (3, 4096, False), (2, 16400, True),
+                                           # a warp a row of several pieces
+                                           (1195, 528, True), (1190, 2048, False),
+                                           (1186, 2576, True)])
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("ckpt", [False, True])
 def test_silu_mul(rows, N, concat, weighted, ckpt):
@@ -446,7 +469,7 @@ def test_silu_mul(rows, N, concat, weighted, ckpt):
 
 
 @pytest.mark.parametrize("T,k,E,N,concat", [(1, 8, 8, 256, False), (29, 3, 6, 528, True),
-                                            (50, 4, 9, 1024, False)])
+                                            (50, 4, 9, 1024, False), (700, 2, 5, 784, True)])
 def test_silu_mul_by_assignment(T, k, E, N, concat):
     """row_of and weights in the order of the gate equal the same weights by row, bit for bit;
     dropped slots (weights NaN) get gradient 0, an entry past the rows in use is flagged."""
