@@ -7,6 +7,11 @@ as None are allocated, uninitialised, for the stream that the call runs on). ``g
 ``dispatch``, ``swiglu``, ``expert_mlp`` and ``combine`` are the same operators with autograd, to
 stand beside ``grouped_mm``; they run on the current stream, and their backward passes do not
 support being differentiated again.
+
+Capture in a CUDA graph: the calls that write into buffers need nothing but their buffers. A
+backward pass of the autograd forms can be captured like any other of torch: together with its
+forward pass, and while no eager graph of the same leaves lives (torch ties a leaf's gradient to
+the stream of the graph that used it first, and a capture cannot wait for that stream).
 """
 from __future__ import annotations
 
@@ -57,11 +62,15 @@ def _arg(t, name, shape, dtype, dev) -> Optional[int]:
     one. One combined test for the usual case, the messages of ``_check`` for the others."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
-            and t.get_device() == dev and t.is_contiguous()):
-        _check(t, name, dtype, len(shape))
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _check(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -149,13 +158,14 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
 
 # ---------------------------------------------------------------------------------- unroute
 
-def _tokens(row_of, k):
+def _tokens(row_of, k, dev):
     """(tokens, k, address) of row_of."""
-    _check(row_of, "row_of", _I32, 1)
-    k, n = int(k), row_of.numel()
-    if k < 1 or n % k != 0:
+    n = row_of.numel() if isinstance(row_of, torch.Tensor) else 0
+    rp = _arg(row_of, "row_of", (n,), _I32, dev)
+    k = int(k)
+    if rp is None or k < 1 or n % k != 0:
         raise ValueError("row_of must hold k entries for each token")
-    return n // k, k, row_of.data_ptr()
+    return n // k, k, rp
 
 
 def unroute(Y: torch.Tensor, row_of: torch.Tensor, k: int, out: Optional[torch.Tensor] = None, *,
@@ -167,9 +177,9 @@ def unroute(Y: torch.Tensor, row_of: torch.Tensor, k: int, out: Optional[torch.T
     Y bf16 [rows, N]; row_of int32 [T*k] from ``route`` (-1 adds nothing); weights float32 [T, k]
     (None: 1); residual bf16 [T, N] (None: 0; may be ``out``); out bf16 [T, N]."""
     _check(Y, "Y", _BF16, 2)
-    T, k, rp = _tokens(row_of, k)
-    rows, N = Y.shape
     dev = Y.get_device()
+    T, k, rp = _tokens(row_of, k, dev)
+    rows, N = Y.shape
     out = _new(out, (T, N), _BF16, Y, stream)
     rc = lib().gg_unroute(Y.data_ptr(), rows, rp, _arg(weights, "weights", (T, k), _F32, dev),
                           _arg(residual, "residual", (T, N), _BF16, dev), T, k, N,
@@ -191,7 +201,8 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
     those past the last of ``offs`` become zeros. row_of's rows must be distinct. Returns
     (dY, dweights)."""
     _check(dout, "dout", _BF16, 2)
-    T, k, rp = _tokens(row_of, k)
+    dev = dout.get_device()
+    T, k, rp = _tokens(row_of, k, dev)
     N = dout.shape[1]
     if dout.shape[0] != T:
         raise ValueError("dout must have a row for each token")
@@ -200,7 +211,6 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
     if dweights is not None and Y is None:
         raise ValueError("dweights needs Y")
     rows = (dY if dY is not None else Y).shape[0]
-    dev = dout.get_device()
     rc = lib().gg_unroute_backward(
         dout.data_ptr(), _arg(Y, "Y", (rows, N), _BF16, dev), rows, rp,
         _arg(weights, "weights", (T, k), _F32, dev), T, k, N, _used_ptr(offs, zero_tail),
@@ -479,8 +489,9 @@ def swiglu(H: torch.Tensor, offs: torch.Tensor, *, row_of: Optional[torch.Tensor
            ckpt8: bool = False, status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``silu_mul`` with the gradients of H and of the weights; rows past the last offset are
     zero in the result and in dH (a row_of names every row before it, as ``route``'s does; to
-    drop an assignment, drop its id before ``route``). With ``ckpt8`` H is kept for the backward pass in 8 bits
-    (e4m3, a power-of-two scale for 32 columns), and the gradients are those at these values."""
+    drop an assignment, drop its id before ``route``). With ``ckpt8`` H is kept for the backward
+    pass in 8 bits (e4m3, a power-of-two scale for 32 columns), and the gradients are those at
+    these values."""
     if _wants_grad(H, weights):
         return _SwiGLU.apply(H, offs, row_of, weights, gate_up_concat, ckpt8, status)
     return silu_mul(H, offs=offs, row_of=row_of, weights=weights, gate_up_concat=gate_up_concat,

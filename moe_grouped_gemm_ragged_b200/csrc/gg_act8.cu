@@ -2,6 +2,7 @@
 // the 8-bit row form, and the backward pass that starts from that form (or from the bf16
 // input). And the form itself: packed rows to 8 bits and back.
 #include <cstdint>
+#include <type_traits>
 
 #include "gg_ops.cuh"
 
@@ -56,20 +57,24 @@ __device__ __forceinline__ float2 sigmoid(const float2& x) {
   return t;
 }
 
-// A row belongs to W warps of a block (1 or all), which take its 32-vector pieces in turn, U
-// pieces at once: their loads are in flight together.
-template <int W>
+// A row belongs to G lanes of a warp (W 1), or to all W warps of a block (G 32). They take its
+// pieces of G vectors in turn, U pieces at once: their loads are in flight together.
+template <int G, int W>
 __device__ __forceinline__ int64_t my_item() {
-  return (int64_t)blockIdx.x * (WARPS / W) + (threadIdx.x >> 5) / W;
+  return W == 1 ? (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G : blockIdx.x;
 }
-template <int W, int U>
+template <int G, int W, int U>
 __device__ __forceinline__ int first_vec() {
-  return (threadIdx.x >> 5) % W * U * 32 + (threadIdx.x & 31);
+  return (W == 1 ? 0 : (threadIdx.x >> 5) * U * G) + threadIdx.x % G;
 }
-// One thread of the row's warps.
-template <int W>
+// The lanes that work on the row together, and the first thread of the row's.
+template <int G>
+__device__ __forceinline__ uint32_t row_mask() {
+  return G == 32 ? ALL : ((1u << (G & 31)) - 1u) << ((threadIdx.x & 31) / G * G);
+}
+template <int G, int W>
 __device__ __forceinline__ bool leader() {
-  return threadIdx.x % (W * 32) == 0;
+  return threadIdx.x % (G * W) == 0;
 }
 
 // Packed row of item b (an assignment, or a row), -1 for a dropped assignment; *live: the row
@@ -106,7 +111,7 @@ __device__ __forceinline__ int64_t up_code(const Params& p, int c) {
   return p.concat ? (c >> 2) + (p.half + kBlock - 1) / kBlock : gate_code(p, c) + 4;
 }
 
-template <int W, int U, bool CKPT>
+template <int G, int W, int U, bool CKPT>
 __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
   const int vecs = p.half / 8;
   const int64_t used =
@@ -115,37 +120,37 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
     clear_tail(p, used, p.act, vecs);
     return;
   }
-  const int64_t item = my_item<W>();
+  const int64_t item = my_item<G, W>();
   if (item >= p.n) return;
-  const int64_t row = row_of_item(p, item, used, leader<W>());
+  const int64_t row = row_of_item(p, item, used, leader<G, W>());
   if (row < 0) return;
   const int64_t base = row * 2 * vecs;
   const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
   const float scale = p.weights != nullptr ? p.weights[item] : 1.f;
-  // whole warps go round together: the four lanes of a block exchange their largest values
-  for (int c0 = first_vec<W, U>(); c0 - (int)(threadIdx.x & 31) < vecs; c0 += W * U * 32) {
+  // a row's lanes go round together: the four lanes of a block exchange their largest values
+  for (int c0 = first_vec<G, W, U>(); c0 - (int)(threadIdx.x % G) < vecs; c0 += W * U * G) {
     uint4 gv[U], uv[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int c = c0 + 32 * i;
+      const int c = c0 + G * i;
       gv[i] = uv[i] = make_uint4(0, 0, 0, 0);
       if (c < vecs) {
         gv[i] = __ldcs(p.H + base + gate_vec(p, c));
         uv[i] = __ldcs(p.H + base + up_vec(p, c));
       }
     }
-    if (row >= used) return;  // the whole warp
+    if (row >= used) return;  // the row's lanes together
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int c = c0 + 32 * i;
-      if (c - (int)(threadIdx.x & 31) >= vecs) break;  // the whole warp
+      const int c = c0 + G * i;
+      if (c - (int)(threadIdx.x % G) >= vecs) break;  // the row's lanes together
       float2 g[4], u[4];
       unpack_bf16(gv[i], g);
       unpack_bf16(uv[i], u);
       if constexpr (CKPT) {
         uint32_t cg, cu;
         bool odd;
-        block_codes(gv[i], uv[i], cg, cu, &odd);
+        block_codes(row_mask<G>(), gv[i], uv[i], cg, cu, &odd);
         if (c < vecs) {
           p.H8_out[base + gate_vec(p, c)] = to_e4m3(g, cg, odd);
           p.H8_out[base + up_vec(p, c)] = to_e4m3(u, cu, odd);
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
 
 // h = [g, u] from its 8 bits (or bf16), s the row's weight, q = sigma(g):
 //   dg = s dact u (q + g q (1 - q)),  du = s dact g q,  act = s g q u,  ds = <dact, g q u>
-template <int W, int U, bool FROM8>
+template <int G, int W, int U, bool FROM8>
 __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Params p) {
   __shared__ float part[WARPS];
   const int vecs = p.half / 8;
@@ -178,21 +183,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
     if (p.act != nullptr) clear_tail(p, used, p.act, vecs);
     return;
   }
-  const int64_t item = my_item<W>();
+  const int64_t item = my_item<G, W>();
   if (item >= p.n) return;
-  const int64_t row = row_of_item(p, item, used, leader<W>());
+  const int64_t row = row_of_item(p, item, used, leader<G, W>());
   float2 dots = both(0.f);
   if (row >= 0) {
     const int64_t base = row * 2 * vecs;
     const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
     const float scale = p.weights != nullptr ? p.weights[item] : 1.f;
-    for (int c0 = first_vec<W, U>(); c0 < vecs; c0 += W * U * 32) {
+    for (int c0 = first_vec<G, W, U>(); c0 < vecs; c0 += W * U * G) {
       uint4 gv[U], uv[U], dv[U];
       uint2 g8[U], u8[U];
       uint8_t cg[U], cu[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int c = c0 + 32 * i;
+        const int c = c0 + G * i;
         if (c >= vecs) continue;
         if constexpr (FROM8) {
           g8[i] = __ldcs(p.H8 + base + gate_vec(p, c));
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
       if (row >= used) return;  // the row's warps together
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int c = c0 + 32 * i;
+        const int c = c0 + G * i;
         if (c >= vecs) continue;
         float2 g[4], u[4], d[4], a[4];
         if constexpr (FROM8) {
@@ -243,9 +248,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
   if (p.dweights == nullptr || row >= used) return;
   float dot = dots.x + dots.y;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(ALL, dot, d);
+  for (int d = G / 2; d > 0; d >>= 1) dot += __shfl_xor_sync(row_mask<G>(), dot, d);
   if constexpr (W == 1) {
-    if ((threadIdx.x & 31) == 0) p.dweights[item] = dot;
+    if (leader<G, W>()) p.dweights[item] = dot;
   } else {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
     __syncthreads();
@@ -257,32 +262,32 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
   }
 }
 
-template <int W, int U>
+template <int G, int W, int U>
 __global__ void __launch_bounds__(THREADS, BLOCKS) pack8_kernel(
     const uint4* X, uint2* X8, uint8_t* scale, int64_t rows, int32_t vecs, const int32_t* used,
     int32_t* status) {
   const int64_t n = rows_in_use(used, rows, status, blockIdx.x == 0 && threadIdx.x == 0);
-  const int64_t r = my_item<W>();
+  const int64_t r = my_item<G, W>();
   if (r >= rows) return;
   const int64_t codes = (vecs + 3) / 4;
-  for (int c0 = first_vec<W, U>(); c0 - (int)(threadIdx.x & 31) < vecs; c0 += W * U * 32) {
+  for (int c0 = first_vec<G, W, U>(); c0 - (int)(threadIdx.x % G) < vecs; c0 += W * U * G) {
     uint4 v[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int c = c0 + 32 * i;
+      const int c = c0 + G * i;
       v[i] = c < vecs ? __ldcs(X + r * vecs + c) : make_uint4(0, 0, 0, 0);
     }
     if (r >= n) return;
     constexpr int P = U > 1 ? 2 : 1;  // pieces whose codes are found together
 #pragma unroll
     for (int i = 0; i < U; i += P) {
-      if (c0 + 32 * i - (int)(threadIdx.x & 31) >= vecs) break;  // the whole warp
+      if (c0 + G * i - (int)(threadIdx.x % G) >= vecs) break;  // the row's lanes together
       uint32_t code[2];
       bool odd;
-      block_codes(v[i], v[i + P - 1], code[0], code[P - 1], &odd);
+      block_codes(row_mask<G>(), v[i], v[i + P - 1], code[0], code[P - 1], &odd);
 #pragma unroll
       for (int k = 0; k < P; ++k) {
-        const int c = c0 + 32 * (i + k);
+        const int c = c0 + G * (i + k);
         if (c >= vecs) continue;
         float2 x[4];
         unpack_bf16(v[i + k], x);
@@ -293,20 +298,20 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) pack8_kernel(
   }
 }
 
-template <int W, int U>
+template <int G, int W, int U>
 __global__ void __launch_bounds__(THREADS, BLOCKS) unpack8_kernel(
     const uint2* X8, const uint8_t* scale, uint4* X, int64_t rows, int32_t vecs,
     const int32_t* used, int32_t zero_tail, int32_t* status) {
   const int64_t n = rows_in_use(used, rows, status, blockIdx.x == 0 && threadIdx.x == 0);
-  const int64_t r = my_item<W>();
+  const int64_t r = my_item<G, W>();
   if (r >= rows) return;
   const int64_t codes = (vecs + 3) / 4;
-  for (int c0 = first_vec<W, U>(); c0 < vecs; c0 += W * U * 32) {
+  for (int c0 = first_vec<G, W, U>(); c0 < vecs; c0 += W * U * G) {
     uint2 q[U];
     uint8_t s[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int c = c0 + 32 * i;
+      const int c = c0 + G * i;
       if (c >= vecs) continue;
       q[i] = __ldcs(X8 + r * vecs + c);
       s[i] = scale[r * codes + (c >> 2)];
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) unpack8_kernel(
     if (r >= n && !zero_tail) return;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int c = c0 + 32 * i;
+      const int c = c0 + G * i;
       if (c >= vecs) continue;
       float2 x[4] = {};
       if (r < n) from_e4m3(q[i], code_scale(s[i]), x);
@@ -364,9 +369,20 @@ Params params(int64_t rows, int64_t N, const int32_t* row_of, const float* weigh
   return p;
 }
 
-// Blocks of the launch: for the items, and for the tail where no item stands for its rows.
-unsigned blocks_for(Params* p, bool share, int sms) {
-  const int64_t per = share ? 1 : WARPS;  // items a block
+// Calls f with the lanes a row: as many as hold it in U pieces, four (the lanes of a block of 32
+// columns) to a warp. 262144 rows of 64 columns to 8 bits take 14 us with four lanes, 64 with a
+// warp; SiLU-and-mul of as many rows of 256 columns 55 with eight lanes, 126.
+template <int N> using Int = std::integral_constant<int, N>;
+template <int U, typename F>
+void by_length(int64_t vecs, const F& f) {
+  if (vecs <= 4 * U) f(Int<4>());
+  else if (vecs <= 8 * U) f(Int<8>());
+  else if (vecs <= 16 * U) f(Int<16>());
+  else f(Int<32>());
+}
+
+// Blocks of the launch for `per` items a block; blocks for the tail where rows are cleared.
+unsigned blocks_for(Params* p, int64_t per, int sms) {
   p->tail0 = (p->n + per - 1) / per;
   int64_t tail = 0;
   if (p->zero_tail && p->rows > 0) {
@@ -374,6 +390,36 @@ unsigned blocks_for(Params* p, bool share, int sms) {
     if (tail > 4 * sms) tail = 4 * sms;
   }
   return (unsigned)(p->tail0 + tail);
+}
+
+template <bool CKPT>
+gg_status launch_forward(Params p, int sms, cudaStream_t stream) {
+  if (share_row(p.n, p.half / 8, sms)) {
+    if (const unsigned grid = blocks_for(&p, 1, sms))
+      silu_mul_kernel<32, WARPS, 1, CKPT><<<grid, THREADS, 0, stream>>>(p);
+  } else {
+    by_length<MANY>(p.half / 8, [&](auto g) {
+      constexpr int G = decltype(g)::value;
+      if (const unsigned grid = blocks_for(&p, THREADS / G, sms))
+        silu_mul_kernel<G, 1, MANY, CKPT><<<grid, THREADS, 0, stream>>>(p);
+    });
+  }
+  return launched("gg_silu_mul");
+}
+
+template <bool FROM8>
+gg_status launch_backward(Params p, int sms, cudaStream_t stream) {
+  if (share_row(p.n, p.half / 8, sms)) {
+    if (const unsigned grid = blocks_for(&p, 1, sms))
+      silu_mul_backward_kernel<32, WARPS, 1, FROM8><<<grid, THREADS, 0, stream>>>(p);
+  } else {
+    by_length<MANY_BACKWARD>(p.half / 8, [&](auto g) {
+      constexpr int G = decltype(g)::value;
+      if (const unsigned grid = blocks_for(&p, THREADS / G, sms))
+        silu_mul_backward_kernel<G, 1, MANY_BACKWARD, FROM8><<<grid, THREADS, 0, stream>>>(p);
+    });
+  }
+  return launched("gg_silu_mul_backward");
 }
 
 gg_status check_rows8(const void* X, const void* X8, const void* scale, int64_t rows,
@@ -410,14 +456,8 @@ gg_status gg_silu_mul(const void* H, int64_t rows, int64_t N, const int32_t* row
   p.act = static_cast<uint4*>(act);
   p.H8_out = static_cast<uint2*>(H8);
   p.scale_out = static_cast<uint8_t*>(H8_scale);
-  const bool share = share_row(p.n, p.half / 8, sms);
-  const unsigned grid = blocks_for(&p, share, sms);
-  if (grid == 0) return GG_OK;
-  if (share && H8 != nullptr) silu_mul_kernel<WARPS, 1, true><<<grid, THREADS, 0, stream>>>(p);
-  else if (share) silu_mul_kernel<WARPS, 1, false><<<grid, THREADS, 0, stream>>>(p);
-  else if (H8 != nullptr) silu_mul_kernel<1, MANY, true><<<grid, THREADS, 0, stream>>>(p);
-  else silu_mul_kernel<1, MANY, false><<<grid, THREADS, 0, stream>>>(p);
-  return launched("gg_silu_mul");
+  return H8 != nullptr ? launch_forward<true>(p, sms, stream)
+                       : launch_forward<false>(p, sms, stream);
 }
 
 gg_status gg_silu_mul_backward(const void* dact, const void* H, const void* H8,
@@ -446,16 +486,8 @@ gg_status gg_silu_mul_backward(const void* dact, const void* H, const void* H8,
   p.dH = static_cast<uint4*>(dH);
   p.act = static_cast<uint4*>(act);
   p.dweights = dweights;
-  const bool share = share_row(p.n, p.half / 8, sms);
-  const unsigned grid = blocks_for(&p, share, sms);
-  if (grid == 0) return GG_OK;
-  if (share && H8 != nullptr)
-    silu_mul_backward_kernel<WARPS, 1, true><<<grid, THREADS, 0, stream>>>(p);
-  else if (share) silu_mul_backward_kernel<WARPS, 1, false><<<grid, THREADS, 0, stream>>>(p);
-  else if (H8 != nullptr)
-    silu_mul_backward_kernel<1, MANY_BACKWARD, true><<<grid, THREADS, 0, stream>>>(p);
-  else silu_mul_backward_kernel<1, MANY_BACKWARD, false><<<grid, THREADS, 0, stream>>>(p);
-  return launched("gg_silu_mul_backward");
+  return H8 != nullptr ? launch_backward<true>(p, sms, stream)
+                       : launch_backward<false>(p, sms, stream);
 }
 
 gg_status gg_pack8(const void* X, int64_t rows, int64_t cols, const int32_t* rows_used, void* X8,
@@ -466,12 +498,19 @@ gg_status gg_pack8(const void* X, int64_t rows, int64_t cols, const int32_t* row
   int sms = 0;
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (rows == 0) return GG_OK;
-  const bool share = share_row(rows, cols / 8, sms);
-  const int64_t per = share ? 1 : WARPS;
-  const unsigned grid = (unsigned)((rows + per - 1) / per);
-  (share ? pack8_kernel<WARPS, 1> : pack8_kernel<1, MANY>)<<<grid, THREADS, 0, stream>>>(
-      static_cast<const uint4*>(X), static_cast<uint2*>(X8), static_cast<uint8_t*>(scale), rows,
-      (int32_t)(cols / 8), rows_used, dev_status);
+  const auto go = [&](auto kernel, int64_t per) {
+    kernel<<<(unsigned)((rows + per - 1) / per), THREADS, 0, stream>>>(
+        static_cast<const uint4*>(X), static_cast<uint2*>(X8), static_cast<uint8_t*>(scale), rows,
+        (int32_t)(cols / 8), rows_used, dev_status);
+  };
+  if (share_row(rows, cols / 8, sms)) {
+    go(pack8_kernel<32, WARPS, 1>, 1);
+  } else {
+    by_length<MANY>(cols / 8, [&](auto g) {
+      constexpr int G = decltype(g)::value;
+      go(pack8_kernel<G, 1, MANY>, THREADS / G);
+    });
+  }
   return launched("gg_pack8");
 }
 
@@ -486,12 +525,19 @@ gg_status gg_unpack8(const void* X8, const void* scale, int64_t rows, int64_t co
   int sms = 0;
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (rows == 0) return GG_OK;
-  const bool share = share_row(rows, cols / 8, sms);
-  const int64_t per = share ? 1 : WARPS;
-  const unsigned grid = (unsigned)((rows + per - 1) / per);
-  (share ? unpack8_kernel<WARPS, 1> : unpack8_kernel<1, MANY>)<<<grid, THREADS, 0, stream>>>(
-      static_cast<const uint2*>(X8), static_cast<const uint8_t*>(scale), static_cast<uint4*>(X),
-      rows, (int32_t)(cols / 8), rows_used, flags & GG_FLAG_ZERO_TAIL, dev_status);
+  const auto go = [&](auto kernel, int64_t per) {
+    kernel<<<(unsigned)((rows + per - 1) / per), THREADS, 0, stream>>>(
+        static_cast<const uint2*>(X8), static_cast<const uint8_t*>(scale), static_cast<uint4*>(X),
+        rows, (int32_t)(cols / 8), rows_used, flags & GG_FLAG_ZERO_TAIL, dev_status);
+  };
+  if (share_row(rows, cols / 8, sms)) {
+    go(unpack8_kernel<32, WARPS, 1>, 1);
+  } else {
+    by_length<MANY>(cols / 8, [&](auto g) {
+      constexpr int G = decltype(g)::value;
+      go(unpack8_kernel<G, 1, MANY>, THREADS / G);
+    });
+  }
   return launched("gg_unpack8");
 }
 

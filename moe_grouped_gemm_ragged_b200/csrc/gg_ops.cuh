@@ -103,19 +103,20 @@ __device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
 }
 
 // Codes of two blocks: four neighbouring lanes hold the 32 columns of each, eight in `a` and
-// eight in `b`. The whole warp calls; *odd (the same for the warp): some value is not finite.
-__device__ __forceinline__ void block_codes(const uint4& a, const uint4& b, uint32_t& ca,
-                                            uint32_t& cb, bool* odd) {
+// eight in `b`. The lanes of `mask` call together; *odd (the same for them): some value is not
+// finite.
+__device__ __forceinline__ void block_codes(uint32_t mask, const uint4& a, const uint4& b,
+                                            uint32_t& ca, uint32_t& cb, bool* odd) {
   constexpr uint32_t M = 0x7fff7fffu;
-  const auto over_block = [](uint32_t ma, uint32_t mb) {
+  const auto over_block = [mask](uint32_t ma, uint32_t mb) {
     // the halves of ma against one another in the low half, those of mb in the high half
     uint32_t m = __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = __vmaxu2(m, __shfl_xor_sync(mask, m, 1));
+    return __vmaxu2(m, __shfl_xor_sync(mask, m, 2));
   };
   uint32_t m = over_block(__vmaxu2(__vmaxu2(a.x & M, a.y & M), __vmaxu2(a.z & M, a.w & M)),
                           __vmaxu2(__vmaxu2(b.x & M, b.y & M), __vmaxu2(b.z & M, b.w & M)));
-  *odd = __any_sync(0xffffffffu, ((m + 0x00800080u) & 0x80008000u) != 0);
+  *odd = __any_sync(mask, ((m + 0x00800080u) & 0x80008000u) != 0);
   if (*odd)
     m = over_block(__vmaxu2(__vmaxu2(finite_bits(a.x), finite_bits(a.y)),
                             __vmaxu2(finite_bits(a.z), finite_bits(a.w))),
