@@ -2,6 +2,7 @@
 // logits, and the gradient of the logits from the gradient of the weights. A group of 4 to 32
 // lanes takes a token, each lane 8 or more neighbouring experts: their logits are one or two
 // wide loads and stay in registers. What bounds these kernels is instructions, not bytes.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -523,9 +524,9 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 //   sigmoid renormalised  dx_i = v_i (1 - s_i) (g_i - sum g v)
 // The scores are computed again from the logits; dx of a logit that was not chosen is 0 but for
 // the first form. A slot of id -1 carries nothing. A row in shared memory brings the slots to
-// their experts' lanes: it takes g (first form) or dx (the others), slot after slot, so that
-// slots of the same expert add up in their order (finding equal slots first and adding the others
-// at once took longer: 9.5 us against 8.3 for 32768 x 64 top 8).
+// their experts' lanes: it takes g (first form) or dx (the others); slots of the same expert
+// add up in their order. What bounds the kernel is the chain of these steps: a GPU full of tokens
+// is one wave.
 template <typename L, int G, int NV>
 __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool sigmoid,
                                                                 bool renorm, bool wide) {
@@ -548,61 +549,69 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
     *reinterpret_cast<float4*>(d + (j * G + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false;
   float m = -INFINITY;
+#pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
     int32_t id = p.ids[t * p.k + s];
-    if (id >= p.E) {
-      bad = true;
-      id = -1;
-    }
-    float g = 0.f;
-    if (id >= 0) {
+    float g = p.scale * p.dweights[t * p.k + s];
+    bad |= id >= p.E;
+    if (id < 0 || id >= p.E) id = -1, g = 0.f;
+    if (!full && id >= 0) {
       bool ignored = false;
       const float xs = logit_or_mask(to_float(row[id]), &ignored);
-      if (xs > -INFINITY) {
-        g = p.scale * p.dweights[t * p.k + s];
-        m = fmaxf(m, sigmoid ? fminf(xs, 0.f) : xs);
-        c.x[s] = xs;
-      } else {
-        id = -1;
-      }
+      c.x[s] = xs;
+      if (xs > -INFINITY) m = fmaxf(m, sigmoid ? fminf(xs, 0.f) : xs);
+      else id = -1;
     }
     c.id[s] = id;
     c.score[s] = g;
   }
-  m = group_max<G>(mask, m);
-  if (m > -INFINITY) {  // some slot carries something
-    if (!full) {
-      float total = 0.f, mean = 0.f;
+  if (!full) {
+    float total = 1.f, mean = 0.f;
+    if (renorm) {
+      m = group_max<G>(mask, m);
+      total = 0.f;
+#pragma unroll 1
       for (int s = lane; s < p.k; s += G) {
         if (c.id[s] < 0) continue;
-        const float v = renorm ? (sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m))
-                               : sigmoid_over(c.x[s], 0.f);
+        const float v = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
         total += v;
         mean = fmaf(c.score[s], v, mean);
       }
-      total = renorm ? group_sum<G>(mask, total) : 1.f;
-      mean = renorm ? group_sum<G>(mask, mean) / total : 0.f;
-      for (int s = lane; s < p.k; s += G) {
-        if (c.id[s] < 0) continue;
-        const float xs = c.x[s];
-        float v = renorm ? (sigmoid ? sigmoid_over(xs, m) : expf(xs - m)) / total
-                         : sigmoid_over(xs, 0.f);
-        if (sigmoid) v *= sigmoid_over(-xs, 0.f);  // 1 - sigma(x) = sigma(-x)
-        c.score[s] = v * (c.score[s] - mean);
+      total = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 1e-30f));  // 0: no slot
+      mean = group_sum<G>(mask, mean) * total;
+    }
+#pragma unroll 1
+    for (int s = lane; s < p.k; s += G) {
+      if (c.id[s] < 0) continue;
+      const float xs = c.x[s];
+      float v = !renorm ? sigmoid_over(xs, 0.f)
+                        : (sigmoid ? sigmoid_over(xs, m) : expf(xs - m)) * total;
+      if (sigmoid) v *= sigmoid_over(-xs, 0.f);  // 1 - sigma(x) = sigma(-x)
+      c.score[s] = v * (c.score[s] - mean);
+    }
+  }
+  __syncwarp(mask);
+  for (int s0 = 0; s0 < p.k; s0 += G) {
+    const int s = s0 + lane, n = min(p.k - s0, G);
+    const int32_t id = s < p.k ? c.id[s] : -1;
+    const float v = s < p.k ? c.score[s] : 0.f;
+    // expert id is place i of lane id / NV
+    const int i = id % NV;
+    float* place = d + ((i / 4) * G + id / NV) * 4 + i % 4;
+    bool again = false;  // an earlier slot has the same expert
+    for (int q = 0; q + 1 < n; ++q) {
+      const int32_t other = __shfl_sync(mask, id, q, G);
+      again |= q < lane && other == id;
+    }
+    again = again && id >= 0;
+    if (id >= 0 && !again) *place += v;
+    if (__any_sync(mask, again)) {  // such ids do not come from gate_topk
+      for (int q = 1; q < n; ++q) {
+        __syncwarp(mask);
+        if (q == lane && again) *place += v;
       }
     }
     __syncwarp(mask);
-    for (int s = 0; s < p.k; ++s) {
-      if (s % G == lane) {
-        const int id = c.id[s];
-        // expert id is place i of lane id / NV
-        if (id >= 0) {
-          const int i = id % NV;
-          d[((i / 4) * G + id / NV) * 4 + i % 4] += c.score[s];
-        }
-      }
-      __syncwarp(mask);
-    }
   }
   float out[NV];
 #pragma unroll
@@ -610,19 +619,19 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
     const float4 v = *reinterpret_cast<const float4*>(d + (j * G + lane) * 4);
     out[4 * j] = v.x, out[4 * j + 1] = v.y, out[4 * j + 2] = v.z, out[4 * j + 3] = v.w;
   }
-  if (full && m > -INFINITY) {
+  if (full) {
     bool ignored = false;
     float top = -INFINITY, total = 0.f, mean = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) top = fmaxf(top, x[j] = logit_or_mask(x[j], &ignored));
-    top = group_max<G>(mask, top);
+    top = fmaxf(group_max<G>(mask, top), -FLT_MAX);  // all of them masked: every share is 0
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      x[j] = x[j] > -INFINITY ? expf(x[j] - top) : 0.f;
+      x[j] = expf(x[j] - top);
       total += x[j];
       mean = fmaf(x[j], out[j], mean);
     }
-    const float inv = 1.f / group_sum<G>(mask, total);
+    const float inv = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 1e-30f));
     mean = group_sum<G>(mask, mean) * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j) out[j] = x[j] * inv * (out[j] - mean);
