@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
   }
   const int64_t item = my_item<G, W>();
   if (item >= p.n) return;
+  const float scale = p.weights != nullptr ? p.weights[item] : 1.f;  // on its way with the row
   const int64_t row = row_of_item(p, item, used, leader<G, W>());
   if (row < 0) return;
   const int64_t base = row * 2 * vecs;
   const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
-  const float scale = p.weights != nullptr ? p.weights[item] : 1.f;
   // a row's lanes go round together: the four lanes of a block exchange their largest values
   for (int c0 = first_vec<G, W, U>(); c0 - (int)(threadIdx.x % G) < vecs; c0 += W * U * G) {
     uint4 gv[U], uv[U];
@@ -185,12 +185,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
   }
   const int64_t item = my_item<G, W>();
   if (item >= p.n) return;
+  const float scale = p.weights != nullptr ? p.weights[item] : 1.f;  // on its way with the row
   const int64_t row = row_of_item(p, item, used, leader<G, W>());
   float2 dots = both(0.f);
   if (row >= 0) {
     const int64_t base = row * 2 * vecs;
     const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
-    const float scale = p.weights != nullptr ? p.weights[item] : 1.f;
     for (int c0 = first_vec<G, W, U>(); c0 < vecs; c0 += W * U * G) {
       uint4 gv[U], uv[U], dv[U];
       uint2 g8[U], u8[U];

@@ -40,7 +40,7 @@ struct Params {
 // backward of the first two 435 (239) and 265 (205).
 constexpr int BLOCKS = 4;
 
-// Rows and weights of SLOTS slots from s0 on of the tokens from t0 on: negative and 0 for a
+// Rows and weights of SLOTS slots from s0 on of the tokens from t0 on; the row is negative for a
 // dropped assignment, one past `rows`, or one that there is not. Each lane fetches one, the warp
 // shares them. Called by whole warps.
 template <int SLOTS, int PER>
@@ -55,11 +55,11 @@ __device__ __forceinline__ void slots_of(const Params& p, int64_t t0, int s0, in
   float weight = 0.f;
   if (t < p.T && s < p.k) {
     row = p.row_of[t * p.k + s];
+    weight = p.weights != nullptr ? p.weights[t * p.k + s] : 1.f;  // on its way with the row
     if (row >= rows) {
       if (report && threadIdx.x % 32 < N) flag(p.status, GG_DEV_BAD_ROUTE);
       row = -1;
     }
-    if (row >= 0) weight = p.weights != nullptr ? p.weights[t * p.k + s] : 1.f;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -79,18 +79,18 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) unroute_kernel(Params p, int3
   const bool in = v < p.vecs;
   float acc[8] = {};
   for (int s0 = 0; s0 < p.k; s0 += SLOTS) {
-    int32_t r[PER * SLOTS];
-    float w[PER * SLOTS];
-    slots_of<SLOTS, PER>(p, t0, s0, p.rows, chunk == 0 && threadIdx.x < 32, r, w);
     uint4 y[PER * SLOTS], res[PER];
-#pragma unroll
-    for (int i = 0; i < PER * SLOTS; ++i)
-      if (in && r[i] >= 0) y[i] = __ldcs(p.Y + (int64_t)r[i] * p.vecs + v);  // read once
     if constexpr (RESIDUAL) {
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (in && t0 + i < p.T && s0 + SLOTS >= p.k) res[i] = p.residual[(t0 + i) * p.vecs + v];
     }
+    int32_t r[PER * SLOTS];
+    float w[PER * SLOTS];
+    slots_of<SLOTS, PER>(p, t0, s0, p.rows, chunk == 0 && threadIdx.x < 32, r, w);
+#pragma unroll
+    for (int i = 0; i < PER * SLOTS; ++i)
+      if (in && r[i] >= 0) y[i] = __ldcs(p.Y + (int64_t)r[i] * p.vecs + v);  // read once
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
 #pragma unroll
