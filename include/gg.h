@@ -342,7 +342,7 @@ GG_API gg_status gg_unroute_backward(const void* dout, const void* Y, int64_t ro
  * Rows: r < *rows_used (int32, device, e.g. &offs[E-1]; NULL: all rows), weight = weights[r];
  * or, with row_of int32 [n_assign], r = row_of[i] and weight = weights[i] for assignment i (the
  * routing weights in the order of gg_gate_topk; entries distinct or -1, below *rows_used where
- * that is given). weights NULL: 1. Other rows reach no result and are not written, but with
+ * that is given; n_assign 0 names no row). weights NULL: 1. Other rows reach no result and are not written, but with
  * GG_FLAG_ZERO_TAIL the rows of act at and past *rows_used become +0.0.
  *   act bf16 [rows, I]; H8 e4m3 [rows, N] in the columns' order of H and H8_scale uint8
  *   [rows, 2 * ceil(I / 32)] (both or neither NULL): the 8-bit form of gg_pack8, with blocks of

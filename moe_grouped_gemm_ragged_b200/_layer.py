@@ -227,14 +227,16 @@ def _half_blocks(N):
     return 2 * ((N // 2 + BLOCK8 - 1) // BLOCK8)
 
 
-def _act_args(rows, offs, row_of, weights, gate_up_concat, zero_tail):
-    """(rows_used, row_of, n_assign, weights, flags): pointers and sizes of the C call."""
+def _act_args(first, offs, row_of, weights, gate_up_concat, zero_tail):
+    """(rows_used, row_of, n_assign, weights, flags): pointers and sizes of the C call, whose
+    first argument is the rows ``first``."""
+    rows = first.shape[0]
     used = _used_ptr(offs, zero_tail)
     n, rp, na = rows, None, 0
     if row_of is not None:
         _check(row_of, "row_of", _I32, 1)
         n = na = row_of.numel()
-        rp = row_of.data_ptr()
+        rp = row_of.data_ptr() or first.data_ptr()  # of no assignment: not NULL, not read
     return (used, rp, na, _per_row(weights, "weights", n),
             (FLAG_ZERO_TAIL if zero_tail else 0) | (FLAG_GATE_UP_CONCAT if gate_up_concat else 0))
 
@@ -276,7 +278,7 @@ def silu_mul(H: torch.Tensor, act: Optional[torch.Tensor] = None, *,
     _check(H, "H", _BF16, 2)
     rows, N = H.shape
     dev = H.get_device()
-    used, rp, n, wp, flags = _act_args(rows, offs, row_of, weights, gate_up_concat, zero_tail)
+    used, rp, n, wp, flags = _act_args(H, offs, row_of, weights, gate_up_concat, zero_tail)
     p8, ps = _args8(H8, H8_scale, rows, N, _half_blocks(N), dev)
     act = _new(act, (rows, N // 2), _BF16, H, stream)
     rc = lib().gg_silu_mul(H.data_ptr(), rows, N, used, rp, n, wp, flags,
@@ -305,7 +307,7 @@ def silu_mul_backward(dact: torch.Tensor, dH: Optional[torch.Tensor] = None, *,
     N, dev = 2 * half, dact.get_device()
     if (H is None) == (H8 is None):
         raise ValueError("exactly one of H and H8 must be given")
-    used, rp, n, wp, flags = _act_args(rows, offs, row_of, weights, gate_up_concat, zero_tail)
+    used, rp, n, wp, flags = _act_args(dact, offs, row_of, weights, gate_up_concat, zero_tail)
     p8, ps = _args8(H8, H8_scale, rows, N, _half_blocks(N), dev)
     dH = _new(dH, (rows, N), _BF16, dact, stream)
     rc = lib().gg_silu_mul_backward(

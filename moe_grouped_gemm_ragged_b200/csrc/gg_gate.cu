@@ -1,7 +1,7 @@
 // The gate before the routing: each token's k experts and their weights from the router's
 // logits, and the gradient of the logits from the gradient of the weights. A group of 4 to 32
-// lanes takes a token, each lane 8 or more neighbouring experts: their logits are one or two
-// wide loads and stay in registers. What bounds these kernels is instructions, not bytes.
+// lanes takes a token, each lane 2 to 32 neighbouring experts: their logits are a few wide loads
+// and stay in registers. What bounds these kernels is instructions, not bytes.
 #include <cfloat>
 #include <cmath>
 #include <cstdint>

@@ -508,6 +508,21 @@ def test_silu_mul_by_assignment(T, k, E, N, concat):
     assert int(st.item()) == gg.DEV_BAD_ROUTE
 
 
+def test_silu_mul_of_no_assignment():
+    """An empty row_of names no row, whatever the rows in use are; the tail is cleared all the
+    same."""
+    H, d = (torch.randn(6, n, device="cuda").to(torch.bfloat16) for n in (256, 128))
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    offs = torch.tensor([4], dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(offs=offs), dict(offs=offs, zero_tail=True)):
+        act = gg.silu_mul(H, sentinel((6, 128)), row_of=none, **kw)
+        dH = gg.silu_mul_backward(d, sentinel((6, 256)), H=H, row_of=none, **kw)
+        kept = 4 if "zero_tail" in kw else 6
+        for t in (act, dH):
+            assert bool(is_sentinel(t[:kept]).all())
+            assert bool((t[kept:].view(torch.int16) == 0).all())
+
+
 # ---------------------------------------------------------------------------- run together
 
 def _layer_inputs(T=96, K=256, E=8, k=3, N=512, K2=256, seed=17):
