@@ -113,6 +113,7 @@ __device__ __forceinline__ int64_t up_code(const Params& p, int c) {
 
 template <int G, int W, int U, bool CKPT>
 __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
+  after_previous();
   const int vecs = p.half / 8;
   const int64_t used =
       rows_in_use(p.used, p.rows, p.status, blockIdx.x == 0 && threadIdx.x == 0);
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
 //   dg = s dact u (q + g q (1 - q)),  du = s dact g q,  act = s g q u,  ds = <dact, g q u>
 template <int G, int W, int U, bool FROM8>
 __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Params p) {
+  after_previous();
   __shared__ float part[WARPS];
   const int vecs = p.half / 8;
   const int64_t used =
@@ -266,6 +268,7 @@ template <int G, int W, int U>
 __global__ void __launch_bounds__(THREADS, BLOCKS) pack8_kernel(
     const uint4* X, uint2* X8, uint8_t* scale, int64_t rows, int32_t vecs, const int32_t* used,
     int32_t* status) {
+  after_previous();
   const int64_t n = rows_in_use(used, rows, status, blockIdx.x == 0 && threadIdx.x == 0);
   const int64_t r = my_item<G, W>();
   if (r >= rows) return;
@@ -302,6 +305,7 @@ template <int G, int W, int U>
 __global__ void __launch_bounds__(THREADS, BLOCKS) unpack8_kernel(
     const uint2* X8, const uint8_t* scale, uint4* X, int64_t rows, int32_t vecs,
     const int32_t* used, int32_t zero_tail, int32_t* status) {
+  after_previous();
   const int64_t n = rows_in_use(used, rows, status, blockIdx.x == 0 && threadIdx.x == 0);
   const int64_t r = my_item<G, W>();
   if (r >= rows) return;
@@ -394,32 +398,38 @@ unsigned blocks_for(Params* p, int64_t per, int sms) {
 
 template <bool CKPT>
 gg_status launch_forward(Params p, int sms, cudaStream_t stream) {
+  gg_status s = GG_OK;
+  const auto go = [&](auto kernel, int64_t per) {
+    if (const unsigned grid = blocks_for(&p, per, sms))
+      s = launch("gg_silu_mul", kernel, grid, THREADS, stream, p);
+  };
   if (share_row(p.n, p.half / 8, sms)) {
-    if (const unsigned grid = blocks_for(&p, 1, sms))
-      silu_mul_kernel<32, WARPS, 1, CKPT><<<grid, THREADS, 0, stream>>>(p);
+    go(silu_mul_kernel<32, WARPS, 1, CKPT>, 1);
   } else {
     by_length<MANY>(p.half / 8, [&](auto g) {
       constexpr int G = decltype(g)::value;
-      if (const unsigned grid = blocks_for(&p, THREADS / G, sms))
-        silu_mul_kernel<G, 1, MANY, CKPT><<<grid, THREADS, 0, stream>>>(p);
+      go(silu_mul_kernel<G, 1, MANY, CKPT>, THREADS / G);
     });
   }
-  return launched("gg_silu_mul");
+  return s;
 }
 
 template <bool FROM8>
 gg_status launch_backward(Params p, int sms, cudaStream_t stream) {
+  gg_status s = GG_OK;
+  const auto go = [&](auto kernel, int64_t per) {
+    if (const unsigned grid = blocks_for(&p, per, sms))
+      s = launch("gg_silu_mul_backward", kernel, grid, THREADS, stream, p);
+  };
   if (share_row(p.n, p.half / 8, sms)) {
-    if (const unsigned grid = blocks_for(&p, 1, sms))
-      silu_mul_backward_kernel<32, WARPS, 1, FROM8><<<grid, THREADS, 0, stream>>>(p);
+    go(silu_mul_backward_kernel<32, WARPS, 1, FROM8>, 1);
   } else {
     by_length<MANY_BACKWARD>(p.half / 8, [&](auto g) {
       constexpr int G = decltype(g)::value;
-      if (const unsigned grid = blocks_for(&p, THREADS / G, sms))
-        silu_mul_backward_kernel<G, 1, MANY_BACKWARD, FROM8><<<grid, THREADS, 0, stream>>>(p);
+      go(silu_mul_backward_kernel<G, 1, MANY_BACKWARD, FROM8>, THREADS / G);
     });
   }
-  return launched("gg_silu_mul_backward");
+  return s;
 }
 
 gg_status check_rows8(const void* X, const void* X8, const void* scale, int64_t rows,
@@ -499,9 +509,9 @@ gg_status gg_pack8(const void* X, int64_t rows, int64_t cols, const int32_t* row
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (rows == 0) return GG_OK;
   const auto go = [&](auto kernel, int64_t per) {
-    kernel<<<(unsigned)((rows + per - 1) / per), THREADS, 0, stream>>>(
-        static_cast<const uint4*>(X), static_cast<uint2*>(X8), static_cast<uint8_t*>(scale), rows,
-        (int32_t)(cols / 8), rows_used, dev_status);
+    s = launch("gg_pack8", kernel, (unsigned)((rows + per - 1) / per), THREADS, stream,
+               static_cast<const uint4*>(X), static_cast<uint2*>(X8),
+               static_cast<uint8_t*>(scale), rows, (int32_t)(cols / 8), rows_used, dev_status);
   };
   if (share_row(rows, cols / 8, sms)) {
     go(pack8_kernel<32, WARPS, 1>, 1);
@@ -511,7 +521,7 @@ gg_status gg_pack8(const void* X, int64_t rows, int64_t cols, const int32_t* row
       go(pack8_kernel<G, 1, MANY>, THREADS / G);
     });
   }
-  return launched("gg_pack8");
+  return s;
 }
 
 gg_status gg_unpack8(const void* X8, const void* scale, int64_t rows, int64_t cols,
@@ -526,9 +536,10 @@ gg_status gg_unpack8(const void* X8, const void* scale, int64_t rows, int64_t co
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (rows == 0) return GG_OK;
   const auto go = [&](auto kernel, int64_t per) {
-    kernel<<<(unsigned)((rows + per - 1) / per), THREADS, 0, stream>>>(
-        static_cast<const uint2*>(X8), static_cast<const uint8_t*>(scale), static_cast<uint4*>(X),
-        rows, (int32_t)(cols / 8), rows_used, flags & GG_FLAG_ZERO_TAIL, dev_status);
+    s = launch("gg_unpack8", kernel, (unsigned)((rows + per - 1) / per), THREADS, stream,
+               static_cast<const uint2*>(X8), static_cast<const uint8_t*>(scale),
+               static_cast<uint4*>(X), rows, (int32_t)(cols / 8), rows_used,
+               flags & GG_FLAG_ZERO_TAIL, dev_status);
   };
   if (share_row(rows, cols / 8, sms)) {
     go(unpack8_kernel<32, WARPS, 1>, 1);
@@ -538,7 +549,7 @@ gg_status gg_unpack8(const void* X8, const void* scale, int64_t rows, int64_t co
       go(unpack8_kernel<G, 1, MANY>, THREADS / G);
     });
   }
-  return launched("gg_unpack8");
+  return s;
 }
 
 }  // extern "C"

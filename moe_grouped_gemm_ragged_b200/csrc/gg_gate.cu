@@ -382,6 +382,7 @@ __device__ __forceinline__ uint32_t group_mask() {
 template <typename L, int G, int NV, bool BIAS>
 __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, bool renorm,
                                                        bool wide, bool wide_bias) {
+  after_previous();
   constexpr bool EXACT = !BIAS && sizeof(L) == 2;  // the keys hold the whole value
   constexpr int SLOTS = GG_GATE_MAX_K + (EXACT ? 0 : MORE);
   __shared__ Chosen<SLOTS> chosen[THREADS / G];
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 template <typename L, int G, int NV>
 __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool sigmoid,
                                                                 bool renorm, bool wide) {
+  after_previous();
   __shared__ Chosen<GG_GATE_MAX_K> chosen[THREADS / G];
   // four experts of every lane side by side, then the next four: lanes' vectors are neighbours;
   // 16 floats more put the rows of two 4-lane groups into different banks
@@ -661,7 +663,8 @@ void by_experts(int E, bool few, const F& f) {
 constexpr int64_t FEW = 4096;
 
 template <typename L, bool BIAS>
-void launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
+gg_status launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
+  gg_status s = GG_OK;
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16);
   const bool wide_bias = p.E % 8 == 0 && !misaligned(p.bias, 16);
   // sixteen experts a lane and so more tokens a warp for bf16 (7.3 us for 32768 x 64, 8.3 with
@@ -670,19 +673,22 @@ void launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream
   constexpr int MANY = !BIAS && sizeof(L) == 2 ? 16 : 8;
   by_experts<MANY>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
-    gate_kernel<L, G, NV, BIAS><<<(unsigned)((p.T + PER - 1) / PER), THREADS, 0, stream>>>(
-        p, sigmoid, renorm, wide, wide_bias);
+    s = launch("gg_gate_topk", gate_kernel<L, G, NV, BIAS>, (unsigned)((p.T + PER - 1) / PER),
+               THREADS, stream, p, sigmoid, renorm, wide, wide_bias);
   });
+  return s;
 }
 
 template <typename L>
-void launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
+gg_status launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
+  gg_status s = GG_OK;
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16) && !misaligned(p.dlogits, 16);
   by_experts<16>(p.E, false, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
-    gate_backward_kernel<L, G, NV><<<(unsigned)((p.T + PER - 1) / PER), THREADS, 0, stream>>>(
-        p, sigmoid, renorm, wide);
+    s = launch("gg_gate_topk_backward", gate_backward_kernel<L, G, NV>,
+               (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, sigmoid, renorm, wide);
   });
+  return s;
 }
 
 gg_status check(int64_t T, int32_t E, int32_t k, int32_t score, int32_t flags, float scale,
@@ -731,11 +737,11 @@ gg_status gg_gate_topk(const void* logits, int64_t T, int32_t E, int32_t k, cons
   p.k = k;
   p.scale = scale;
   const bool sig = score == GG_GATE_SIGMOID, renorm = (flags & GG_GATE_RENORM) != 0;
-  if (f32 && bias) launch_gate<float, true>(p, sig, renorm, stream);
-  else if (f32) launch_gate<float, false>(p, sig, renorm, stream);
-  else if (bias) launch_gate<__nv_bfloat16, true>(p, sig, renorm, stream);
-  else launch_gate<__nv_bfloat16, false>(p, sig, renorm, stream);
-  return launched("gg_gate_topk");
+  if (f32)
+    return bias != nullptr ? launch_gate<float, true>(p, sig, renorm, stream)
+                           : launch_gate<float, false>(p, sig, renorm, stream);
+  return bias != nullptr ? launch_gate<__nv_bfloat16, true>(p, sig, renorm, stream)
+                         : launch_gate<__nv_bfloat16, false>(p, sig, renorm, stream);
 }
 
 gg_status gg_gate_topk_backward(const void* logits, int64_t T, int32_t E, int32_t k,
@@ -766,9 +772,8 @@ gg_status gg_gate_topk_backward(const void* logits, int64_t T, int32_t E, int32_
   p.k = k;
   p.scale = scale;
   const bool sig = score == GG_GATE_SIGMOID, renorm = (flags & GG_GATE_RENORM) != 0;
-  if (f32) launch_backward<float>(p, sig, renorm, stream);
-  else launch_backward<__nv_bfloat16>(p, sig, renorm, stream);
-  return launched("gg_gate_topk_backward");
+  return f32 ? launch_backward<float>(p, sig, renorm, stream)
+             : launch_backward<__nv_bfloat16>(p, sig, renorm, stream);
 }
 
 }  // extern "C"

@@ -72,6 +72,7 @@ __device__ __forceinline__ void slots_of(const Params& p, int64_t t0, int s0, in
 // threads PER tokens each. More than SLOTS slots (SLOTS 8, PER 1 only) take several rounds.
 template <int SLOTS, int PER, bool RESIDUAL>
 __global__ void __launch_bounds__(THREADS, BLOCKS) unroute_kernel(Params p, int32_t chunks) {
+  after_previous();
   static_assert(PER == 1 || SLOTS < 8, "one round but for SLOTS 8");
   const int32_t chunk = blockIdx.x % chunks;
   const int64_t t0 = ((int64_t)(blockIdx.x / chunks) * blockDim.y + threadIdx.y) * PER;
@@ -149,6 +150,7 @@ __device__ __forceinline__ int sum_index(int lane) {
 template <int SLOTS, int PER, bool DY, bool DW>
 __global__ void __launch_bounds__(THREADS, BLOCKS) unroute_backward_kernel(Params p,
                                                                            int32_t blocks) {
+  after_previous();
   constexpr int N = PER * SLOTS;
   __shared__ float part[WARPS][N];
   const int64_t used = rows_in_use(p.used, p.rows, p.status,
@@ -239,11 +241,10 @@ gg_status launch_forward(const Params& p, const Shape& s, cudaStream_t stream) {
   const int64_t per = (int64_t)s.block.y * (p.residual != nullptr ? LESS : PER);
   const int64_t grid = (p.T + per - 1) / per * s.chunks;
   if (grid >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
-  if (p.residual != nullptr)
-    unroute_kernel<SLOTS, LESS, true><<<(unsigned)grid, s.block, 0, stream>>>(p, (int)s.chunks);
-  else
-    unroute_kernel<SLOTS, PER, false><<<(unsigned)grid, s.block, 0, stream>>>(p, (int)s.chunks);
-  return launched("gg_unroute");
+  return launch("gg_unroute",
+                p.residual != nullptr ? unroute_kernel<SLOTS, LESS, true>
+                                      : unroute_kernel<SLOTS, PER, false>,
+                (unsigned)grid, s.block, stream, p, (int32_t)s.chunks);
 }
 
 template <int SLOTS, int PER>
@@ -251,15 +252,11 @@ gg_status launch_backward(const Params& p, const Shape& s, int64_t tail, cudaStr
   const int64_t per = (int64_t)s.block.y * PER;
   const int64_t blocks = (p.T + per - 1) / per;
   if (blocks + tail >= (int64_t(1) << 31)) return GG_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)(blocks + tail);
-  const int32_t n = (int32_t)blocks;
-  if (p.dweights == nullptr)
-    unroute_backward_kernel<SLOTS, PER, true, false><<<grid, s.block, 0, stream>>>(p, n);
-  else if (p.dY == nullptr)
-    unroute_backward_kernel<SLOTS, PER, false, true><<<grid, s.block, 0, stream>>>(p, n);
-  else
-    unroute_backward_kernel<SLOTS, PER, true, true><<<grid, s.block, 0, stream>>>(p, n);
-  return launched("gg_unroute_backward");
+  const auto kernel = p.dweights == nullptr ? unroute_backward_kernel<SLOTS, PER, true, false>
+                      : p.dY == nullptr     ? unroute_backward_kernel<SLOTS, PER, false, true>
+                                            : unroute_backward_kernel<SLOTS, PER, true, true>;
+  return launch("gg_unroute_backward", kernel, (unsigned)(blocks + tail), s.block, stream, p,
+                (int32_t)blocks);
 }
 
 gg_status check(int64_t rows, int64_t T, int32_t k, int64_t N, const int32_t* dev_status) {

@@ -837,6 +837,51 @@ def test_captured_layer_step_replays_on_new_inputs():
         assert bool((b["out"][used:].view(torch.int16) == 0).all())
 
 
+def test_chain_of_calls_needs_no_synchronisation():
+    """Each call reads what the one before wrote, on one stream (a kernel may be scheduled while
+    the one before it ends): the same bits as with a synchronisation after every call."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    T, k, E, N = 900, 2, 64, 512
+    x0 = torch.randn(T, E, generator=gen, device="cuda")
+    Y0 = torch.randn(T * k, N, generator=gen, device="cuda").to(torch.bfloat16)
+    row_of = torch.randperm(T * k, generator=gen, device="cuda").to(torch.int32)
+    offs = torch.tensor([T * k - 5], dtype=torch.int32, device="cuda")
+
+    def chain(sync):
+        x, Y, seen = x0.clone(), Y0.clone(), []
+        wait = torch.cuda.synchronize if sync else lambda: None
+        out = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        dY, dw = torch.zeros_like(Y), torch.zeros(T, k, device="cuda")
+        act = torch.zeros(T * k, N // 2, dtype=torch.bfloat16, device="cuda")
+        dH, dx = torch.zeros_like(Y), torch.zeros_like(x)
+        H8 = torch.zeros(T * k, N, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        s8 = torch.zeros(T * k, N // 32, dtype=torch.uint8, device="cuda").view(
+            torch.float8_e8m0fnu)
+        ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+        w = torch.zeros(T, k, device="cuda")
+        for _ in range(6):
+            for call in (lambda: gg.gate_topk(x, k, topk_ids=ids, weights=w),
+                         lambda: gg.unroute(Y, row_of, k, out, weights=w),
+                         lambda: gg.unroute_backward(out, row_of, k, dY, Y=Y, weights=w,
+                                                     dweights=dw),
+                         lambda: gg.gate_topk_backward(x, ids, dw, dx),
+                         lambda: gg.silu_mul(dY, act, offs=offs, H8=H8, H8_scale=s8),
+                         lambda: gg.silu_mul_backward(act, dH, H8=H8, H8_scale=s8, offs=offs),
+                         lambda: gg.pack8(dH, H8, s8, offs=offs),
+                         lambda: gg.unpack8(H8, s8, Y, offs=offs),
+                         lambda: x.add_(dx, alpha=1e-3)):
+                call()
+                wait()
+            seen += [t.clone() for t in (ids, w, out, dw, dx, Y)]
+        torch.cuda.synchronize()
+        return seen
+
+    want = chain(True)
+    for _ in range(3):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_calls_on_another_stream_own_their_buffers():
     """Buffers that a call allocates belong to the stream it runs on; results on a side stream
     equal those on the current one, also while both run."""
