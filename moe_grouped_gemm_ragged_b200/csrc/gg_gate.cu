@@ -35,14 +35,16 @@ struct Params {
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// NV neighbouring logits of a row (first: the lane's first expert); the rest of the lane's
-// share, past E, is masked. wide: E is a multiple of 8 and the rows start on 16 bytes.
+// NV neighbouring logits of a row (first: the lane's first expert, lane * NV); the rest of the
+// lane's share, past E, is masked. wide: E is a multiple of 8 and the rows start on 16 bytes, so
+// that a lane's share does too when its own size is a multiple of that, and no vector reaches
+// past E.
 template <int NV>
 __device__ __forceinline__ void load_row(const float* row, int first, int E, bool wide,
                                          float (&x)[NV]) {
 #pragma unroll
   for (int j = 0; j < NV; j += 4) {
-    if (NV >= 4 && wide && first + j < E) {
+    if ((NV * 4) % 16 == 0 && wide && first + j < E) {
       const float4 v = *reinterpret_cast<const float4*>(row + first + j);
       x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
     } else {
@@ -56,7 +58,7 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* row, int first, in
                                          float (&x)[NV]) {
 #pragma unroll
   for (int j = 0; j < NV; j += 8) {
-    if (NV >= 8 && wide && first + j < E) {
+    if ((NV * 2) % 16 == 0 && wide && first + j < E) {
       float v[8];
       unpack_bf16(*reinterpret_cast<const uint4*>(row + first + j), v);
 #pragma unroll
@@ -70,31 +72,32 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* row, int first, in
 }
 template <int NV>
 __device__ __forceinline__ void store_row(float* row, int first, int E, bool wide,
-                                          const float* x) {
+                                          const float (&x)[NV]) {
 #pragma unroll
   for (int j = 0; j < NV; j += 4) {
-    if (wide && first + j < E) {
-      *reinterpret_cast<float4*>(row + first + j) = *reinterpret_cast<const float4*>(x + j);
+    if ((NV * 4) % 16 == 0 && wide && first + j < E) {
+      *reinterpret_cast<float4*>(row + first + j) =
+          make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
     } else {
 #pragma unroll
-      for (int i = j; i < j + 4; ++i)
+      for (int i = j; i < j + 4 && i < NV; ++i)
         if (first + i < E) row[first + i] = x[i];
     }
   }
 }
 template <int NV>
 __device__ __forceinline__ void store_row(__nv_bfloat16* row, int first, int E, bool wide,
-                                          const float* x) {
+                                          const float (&x)[NV]) {
 #pragma unroll
   for (int j = 0; j < NV; j += 8) {
-    if (wide && first + j < E) {
+    if ((NV * 2) % 16 == 0 && wide && first + j < E) {
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = x[j + i];
       *reinterpret_cast<uint4*>(row + first + j) = pack_bf16(v);
     } else {
 #pragma unroll
-      for (int i = j; i < j + 8; ++i)
+      for (int i = j; i < j + 8 && i < NV; ++i)
         if (first + i < E) row[first + i] = __float2bfloat16_rn(x[i]);
     }
   }
@@ -178,11 +181,14 @@ __device__ __forceinline__ float fast_score(float x, float b) {
 constexpr float CLOSE = 16.f / 8388608.f;
 
 // The order is looked up this many places further than needed, to see that no other expert may
-// belong to the chosen.
-constexpr int MORE = 2;
+// belong to the chosen. Scores under a bias lie closer: with two places about one token in ten
+// thousand of 256 experts stays open, and one such token adds 4 us to a call.
+template <bool BIAS>
+constexpr int MORE = BIAS ? 3 : 2;
 
 template <int SLOTS>
 struct Chosen {  // of one token, in shared memory
+  static constexpr int N = SLOTS;
   int32_t id[SLOTS];
   float x[SLOTS];
   float score[SLOTS];
@@ -250,7 +256,7 @@ __device__ __forceinline__ void order_double(uint32_t mask, int lane, int n, con
   for (int s = lane; s < n; s += G)
     d[s] = double_score<BIAS>(c.x[s], BIAS ? bias[c.id[s]] : 0.f);
   __syncwarp(mask);
-  constexpr int PER = (GG_GATE_MAX_K + MORE + G - 1) / G;
+  constexpr int PER = (C::N + G - 1) / G;
   int32_t id[PER], place[PER];
   float x[PER];
 #pragma unroll
@@ -328,7 +334,7 @@ __device__ __forceinline__ void bf16_keys(uint32_t mask, int first, const __nv_b
   uint32_t w[NV / 2];  // two logits each
 #pragma unroll
   for (int j = 0; j < NV / 2; j += 4) {
-    if (NV >= 8 && wide && first + 2 * j < E) {
+    if ((NV * 2) % 16 == 0 && wide && first + 2 * j < E) {
       const uint4 v = *reinterpret_cast<const uint4*>(row + first + 2 * j);
       w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
     } else {
@@ -374,7 +380,7 @@ __device__ __forceinline__ uint32_t group_mask() {
 
 // Choice by the logit itself without a bias (both scores grow with it, so the choice is
 // exact), by sigma(x) + bias in double precision with one: neighbours of 256 scores are often
-// closer than fp32 tells apart. fp32 logits and fp32 scores are looked up MORE places further
+// closer than fp32 tells apart. fp32 logits and fp32 scores are looked up a few places further
 // than needed, which leaves three cases: each two neighbours are in order for sure (values apart,
 // or equal logits under equal biases, a tie in any precision); some are not, but nothing behind
 // the last one can belong to the first k: those looked up are put in order by doubles; or the
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
                                                        bool wide, bool wide_bias) {
   after_previous();
   constexpr bool EXACT = !BIAS && sizeof(L) == 2;  // the keys hold the whole value
-  constexpr int SLOTS = GG_GATE_MAX_K + (EXACT ? 0 : MORE);
+  constexpr int SLOTS = GG_GATE_MAX_K + (EXACT ? 0 : MORE<BIAS>);
   __shared__ Chosen<SLOTS> chosen[THREADS / G];
   __shared__ double doubles[EXACT ? 1 : THREADS / G][EXACT ? 1 : SLOTS];
   const int lane = threadIdx.x % G;
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
   int got = 0;
   if (t < live_tokens) {
     uint32_t key[NV];
-    const int want = EXACT ? p.k : min(p.k + MORE, p.E);
+    const int want = EXACT ? p.k : min(p.k + MORE<BIAS>, p.E);
     if constexpr (EXACT) {
       bf16_keys<NV>(mask, lane * NV, row, p.E, wide, key, x, &bad);
     } else {
@@ -644,22 +650,30 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// Lanes a token and experts a lane. A warp for each token is the quickest for few of them, NV
-// experts a lane and so several tokens a warp the cheapest in instructions for many.
-template <int NV, typename F>
+// Lanes a token and experts a lane (NV, or half as much again where that wastes less). A warp for
+// each token is the quickest for few of them, several tokens a warp the cheapest in instructions
+// for many. (32768 tokens of 160 and of 384 experts, top 6 and 8, bf16: 18.4 and 34.6 us without
+// the halves in between.)
+template <int NV, int LEAST, typename F>
 void by_experts(int E, bool few, const F& f) {
-  if (few && E <= 64) f(Int<32>(), Int<2>());
+  constexpr int MORE_NV = NV + NV / 2;
+  if (few && E <= 32 * LEAST) f(Int<32>(), Int<LEAST>());
   else if (few && E <= 128) f(Int<32>(), Int<4>());
   else if (few && E <= 256) f(Int<32>(), Int<8>());
   else if (E <= 64) f(Int<64 / NV>(), Int<NV>());
+  else if (E <= 96) f(Int<64 / NV>(), Int<MORE_NV>());
   else if (E <= 128) f(Int<128 / NV>(), Int<NV>());
+  else if (E <= 192) f(Int<128 / NV>(), Int<MORE_NV>());
   else if (E <= 256) f(Int<256 / NV>(), Int<NV>());
+  else if (E <= 384) f(Int<256 / NV>(), Int<MORE_NV>());
   else if (E <= 512) f(Int<32>(), Int<16>());
+  else if (E <= 768) f(Int<32>(), Int<24>());
   else f(Int<32>(), Int<32>());
 }
 
 // 1 x 64 bf16: 2.2 us a call in a graph with a warp a token, 3.3 us with four lanes; 32768 x
 // 64: 16.2 and 7.3 us. The two break even where the warps fill the GPU (148 SMs x 32 or so).
+// Backward 512 x 64: 2.0 and 3.7 us, 4096 x 64 2.9 and 3.9.
 constexpr int64_t FEW = 4096;
 
 template <typename L, bool BIAS>
@@ -671,7 +685,7 @@ gg_status launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t s
   // eight), eight for fp32, whose looking-up further and checking is shared by few tokens anyway
   // (16411 x 256 with a bias: 16.5 us, 19.1 with sixteen)
   constexpr int MANY = !BIAS && sizeof(L) == 2 ? 16 : 8;
-  by_experts<MANY>(p.E, p.T <= FEW, [&](auto g, auto nv) {
+  by_experts<MANY, 2>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
     s = launch("gg_gate_topk", gate_kernel<L, G, NV, BIAS>, (unsigned)((p.T + PER - 1) / PER),
                THREADS, stream, p, sigmoid, renorm, wide, wide_bias);
@@ -683,7 +697,7 @@ template <typename L>
 gg_status launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
   gg_status s = GG_OK;
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16) && !misaligned(p.dlogits, 16);
-  by_experts<16>(p.E, false, [&](auto g, auto nv) {
+  by_experts<16, 4>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
     s = launch("gg_gate_topk_backward", gate_backward_kernel<L, G, NV>,
                (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, sigmoid, renorm, wide);

@@ -87,7 +87,8 @@ def _check_gate(x, k, sigmoid, renorm, scale, bias=None, num=None, flagged=0):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (5, 7, 7), (33, 32, 32), (130, 33, 3),
                                    (257, 64, 1), (64, 160, 6), (40, 256, 8), (9, 257, 5),
-                                   (7, 1024, 32), (3, 1000, 1)])
+                                   (7, 1024, 32), (3, 1000, 1), (30, 96, 4), (30, 192, 8),
+                                   (10, 384, 8), (8, 600, 6), (20, 128, 8)])
 @pytest.mark.parametrize("sigmoid,renorm", [(False, False), (False, True), (True, False),
                                             (True, True)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -103,7 +104,13 @@ def test_gate(T, E, k, sigmoid, renorm, dtype):
                                        (64, 8, torch.bfloat16), (64, 6, torch.float32),
                                        (100, 3, torch.bfloat16), (128, 8, torch.float32),
                                        (160, 8, torch.bfloat16), (256, 6, torch.float32),
-                                       (400, 2, torch.bfloat16), (1000, 32, torch.float32)])
+                                       (400, 2, torch.bfloat16), (1000, 32, torch.float32),
+                                       # half as many experts a lane again
+                                       (72, 8, torch.bfloat16), (96, 3, torch.float32),
+                                       (90, 8, torch.float32), (136, 2, torch.float32),
+                                       (192, 8, torch.bfloat16), (320, 6, torch.float32),
+                                       (384, 8, torch.bfloat16), (264, 32, torch.bfloat16),
+                                       (520, 8, torch.bfloat16), (768, 4, torch.float32)])
 def test_gate_of_many_tokens(E, k, dtype):
     """Several tokens a warp (above 4096), the last group of them short, some not in use."""
     gen = torch.Generator().manual_seed(E)
