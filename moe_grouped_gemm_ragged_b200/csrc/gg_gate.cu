@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
     }
     __syncwarp(mask);
   }
-  float m = 0.f, inv = 1.f;
+  float m = 0.f, total = 1.f;
   if (got > 0 && (renorm || !sigmoid)) {
     // shares: each score over the sum of the chosen (renorm) or of all (softmax), both relative
     // to the largest; without a bias the first has it
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       m = group_max<G>(mask, m);
     }
     if (sigmoid) m = fminf(m, 0.f);
-    float total = 0.f;
+    total = 0.f;
     if (renorm) {
 #pragma unroll 1
       for (int s = lane; s < got; s += G) {
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 #pragma unroll
       for (int j = 0; j < NV; ++j) total += expf(x[j] - m);  // 0 of -inf
     }
-    inv = __fdividef(1.f, group_sum<G>(mask, total));
+    total = group_sum<G>(mask, total);
   }
 #pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
     if (s < got) {
       if (renorm) w = c.score[s];
       else w = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
-      w *= p.scale * inv;
+      w = p.scale * (w / total);  // a true quotient: the share of an only slot is 1
     }
     p.ids[t * p.k + s] = s < got ? c.id[s] : -1;
     p.weights[t * p.k + s] = w;
@@ -534,11 +534,18 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 // their experts' lanes: it takes g (first form) or dx (the others); slots of the same expert
 // add up in their order. What bounds the kernel is the chain of these steps: a GPU full of tokens
 // is one wave.
+struct Slots {  // of one token, in shared memory
+  int32_t id[GG_GATE_MAX_K];
+  float x[GG_GATE_MAX_K];
+  float g[GG_GATE_MAX_K];  // scale * dweights, then dx
+  float v[GG_GATE_MAX_K];
+};
+
 template <typename L, int G, int NV>
 __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool sigmoid,
                                                                 bool renorm, bool wide) {
   after_previous();
-  __shared__ Chosen<GG_GATE_MAX_K> chosen[THREADS / G];
+  __shared__ Slots slots[THREADS / G];
   // four experts of every lane side by side, then the next four: lanes' vectors are neighbours;
   // 16 floats more put the rows of two 4-lane groups into different banks
   __shared__ __align__(16) float rows[THREADS / G][G * NV + 16];
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
   const int64_t t = (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G;
   if (t >= p.T) return;  // the whole group
   const uint32_t mask = group_mask<G>();
-  auto& c = chosen[threadIdx.x / G];  // each lane reads only its own slots
+  Slots& c = slots[threadIdx.x / G];  // each lane reads only its own
   float* d = rows[threadIdx.x / G];
   const L* row = static_cast<const L*>(p.logits) + t * p.E;
   const bool full = !sigmoid && !renorm;
@@ -571,38 +578,41 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
       else id = -1;
     }
     c.id[s] = id;
-    c.score[s] = g;
+    c.g[s] = g;
   }
   if (!full) {
-    float total = 1.f, mean = 0.f;
+    float mean = 0.f;
     if (renorm) {
       m = group_max<G>(mask, m);
-      total = 0.f;
+      float total = 0.f;
 #pragma unroll 1
       for (int s = lane; s < p.k; s += G) {
         if (c.id[s] < 0) continue;
-        const float v = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
-        total += v;
-        mean = fmaf(c.score[s], v, mean);
+        c.v[s] = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
+        total += c.v[s];
       }
-      total = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 1e-30f));  // 0: no slot
-      mean = group_sum<G>(mask, mean) * total;
+      total = group_sum<G>(mask, total);
+#pragma unroll 1
+      for (int s = lane; s < p.k; s += G) {
+        if (c.id[s] < 0) continue;
+        c.v[s] /= total;  // a true quotient: the share of an only slot is 1 and its gradient 0
+        mean = fmaf(c.g[s], c.v[s], mean);
+      }
+      mean = group_sum<G>(mask, mean);
     }
 #pragma unroll 1
     for (int s = lane; s < p.k; s += G) {
       if (c.id[s] < 0) continue;
-      const float xs = c.x[s];
-      float v = !renorm ? sigmoid_over(xs, 0.f)
-                        : (sigmoid ? sigmoid_over(xs, m) : expf(xs - m)) * total;
-      if (sigmoid) v *= sigmoid_over(-xs, 0.f);  // 1 - sigma(x) = sigma(-x)
-      c.score[s] = v * (c.score[s] - mean);
+      float v = renorm ? c.v[s] : sigmoid_over(c.x[s], 0.f);
+      if (sigmoid) v *= sigmoid_over(-c.x[s], 0.f);  // 1 - sigma(x) = sigma(-x)
+      c.g[s] = v * (c.g[s] - mean);
     }
   }
   __syncwarp(mask);
   for (int s0 = 0; s0 < p.k; s0 += G) {
     const int s = s0 + lane, n = min(p.k - s0, G);
     const int32_t id = s < p.k ? c.id[s] : -1;
-    const float v = s < p.k ? c.score[s] : 0.f;
+    const float v = s < p.k ? c.g[s] : 0.f;
     // expert id is place i of lane id / NV
     const int i = id % NV;
     float* place = d + ((i / 4) * G + id / NV) * 4 + i % 4;

@@ -705,6 +705,19 @@ def test_checkpoints_in_8_bits_take_half_the_memory():
     assert kept[1] <= whole * 33 / 64 + (1 << 16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", ["GATE_SOFTMAX", "GATE_SIGMOID"])
+def test_gate_gradient_of_an_only_expert_is_zero(score, dtype):
+    """A renormalised weight of one slot is the scale whatever the logits: no rounding is left."""
+    for T, E in ((5, 16), (300, 64), (5000, 160)):
+        x = 3 * torch.randn(T, E, device="cuda").to(dtype)
+        ids, w = gg.gate_topk(x, 1, score=getattr(gg, score), scale=2.5)
+        assert bool((w == 2.5).all())
+        dx = gg.gate_topk_backward(x, ids, torch.randn_like(w), score=getattr(gg, score),
+                                   scale=2.5)
+        assert bool((dx == 0).all())
+
+
 def test_gate_gradient_of_an_expert_named_twice():
     """ids that gate_topk would not make: both slots add to their expert, in order."""
     x = torch.randn(3, 40, generator=torch.Generator().manual_seed(8))
