@@ -84,16 +84,22 @@ def _new(t, shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _used_ptr(offs, zero_tail):
+def _vector(t, name, dtype, dev):
+    """(address, entries) of a one-dimensional argument of any length."""
+    n = t.numel() if isinstance(t, torch.Tensor) else 0
+    return _arg(t, name, (n,), dtype, dev), n
+
+
+def _used_ptr(offs, zero_tail, dev):
     """Address of the last offset: the number of packed rows in use."""
     if offs is None:
         if zero_tail:
             raise ValueError("zero_tail needs offs")
         return None
-    _check(offs, "offs", _I32, 1)
-    if offs.numel() == 0:
+    p, n = _vector(offs, "offs", _I32, dev)
+    if n == 0:
         raise ValueError("offs must not be empty")
-    return offs.data_ptr() + 4 * (offs.numel() - 1)
+    return p + 4 * (n - 1)
 
 
 # ------------------------------------------------------------------------------------- gate
@@ -160,8 +166,7 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
 
 def _tokens(row_of, k, dev):
     """(tokens, k, address) of row_of."""
-    n = row_of.numel() if isinstance(row_of, torch.Tensor) else 0
-    rp = _arg(row_of, "row_of", (n,), _I32, dev)
+    rp, n = _vector(row_of, "row_of", _I32, dev)
     k = int(k)
     if rp is None or k < 1 or n % k != 0:
         raise ValueError("row_of must hold k entries for each token")
@@ -213,7 +218,7 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
     rows = (dY if dY is not None else Y).shape[0]
     rc = lib().gg_unroute_backward(
         dout.data_ptr(), _arg(Y, "Y", (rows, N), _BF16, dev), rows, rp,
-        _arg(weights, "weights", (T, k), _F32, dev), T, k, N, _used_ptr(offs, zero_tail),
+        _arg(weights, "weights", (T, k), _F32, dev), T, k, N, _used_ptr(offs, zero_tail, dev),
         FLAG_ZERO_TAIL if zero_tail else 0, _arg(dY, "dY", (rows, N), _BF16, dev),
         _arg(dweights, "dweights", (T, k), _F32, dev), _status_ptr(status),
         _stream_handle(stream, dev))
@@ -227,30 +232,28 @@ def _half_blocks(N):
     return 2 * ((N // 2 + BLOCK8 - 1) // BLOCK8)
 
 
-def _act_args(first, offs, row_of, weights, gate_up_concat, zero_tail):
+def _act_args(first, offs, row_of, weights, gate_up_concat, zero_tail, dev):
     """(rows_used, row_of, n_assign, weights, flags): pointers and sizes of the C call, whose
     first argument is the rows ``first``."""
-    rows = first.shape[0]
-    used = _used_ptr(offs, zero_tail)
-    n, rp, na = rows, None, 0
+    used = _used_ptr(offs, zero_tail, dev)
+    n, rp, na = first.shape[0], None, 0
     if row_of is not None:
-        _check(row_of, "row_of", _I32, 1)
-        n = na = row_of.numel()
-        rp = row_of.data_ptr() or first.data_ptr()  # of no assignment: not NULL, not read
-    return (used, rp, na, _per_row(weights, "weights", n),
+        rp, na = _vector(row_of, "row_of", _I32, dev)
+        rp = rp or first.data_ptr()  # of no assignment: not NULL, not read
+        n = na
+    return (used, rp, na, _per_row(weights, "weights", n, dev),
             (FLAG_ZERO_TAIL if zero_tail else 0) | (FLAG_GATE_UP_CONCAT if gate_up_concat else 0))
 
 
-def _per_row(t, name, n):
+def _per_row(t, name, n, dev):
     """float32, one for each assignment (of any shape, e.g. [T, k]) or row."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    _check(t, name, _F32, t.dim())
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} values")
-    return t.data_ptr()
+    return _arg(t, name, t.shape, _F32, dev)
 
 
 def _args8(x8, scale, rows, cols, codes, dev):
@@ -278,7 +281,7 @@ def silu_mul(H: torch.Tensor, act: Optional[torch.Tensor] = None, *,
     _check(H, "H", _BF16, 2)
     rows, N = H.shape
     dev = H.get_device()
-    used, rp, n, wp, flags = _act_args(H, offs, row_of, weights, gate_up_concat, zero_tail)
+    used, rp, n, wp, flags = _act_args(H, offs, row_of, weights, gate_up_concat, zero_tail, dev)
     p8, ps = _args8(H8, H8_scale, rows, N, _half_blocks(N), dev)
     act = _new(act, (rows, N // 2), _BF16, H, stream)
     rc = lib().gg_silu_mul(H.data_ptr(), rows, N, used, rp, n, wp, flags,
@@ -307,14 +310,14 @@ def silu_mul_backward(dact: torch.Tensor, dH: Optional[torch.Tensor] = None, *,
     N, dev = 2 * half, dact.get_device()
     if (H is None) == (H8 is None):
         raise ValueError("exactly one of H and H8 must be given")
-    used, rp, n, wp, flags = _act_args(dact, offs, row_of, weights, gate_up_concat, zero_tail)
+    used, rp, n, wp, flags = _act_args(dact, offs, row_of, weights, gate_up_concat, zero_tail, dev)
     p8, ps = _args8(H8, H8_scale, rows, N, _half_blocks(N), dev)
     dH = _new(dH, (rows, N), _BF16, dact, stream)
     rc = lib().gg_silu_mul_backward(
         dact.data_ptr(), _arg(H, "H", (rows, N), _BF16, dev), p8, ps, rows, N, used, rp, n, wp,
         flags, _arg(dH, "dH", (rows, N), _BF16, dev),
         _arg(act, "act", (rows, half), _BF16, dev),
-        _per_row(dweights, "dweights", rows if row_of is None else n), _status_ptr(status),
+        _per_row(dweights, "dweights", rows if row_of is None else n, dev), _status_ptr(status),
         _stream_handle(stream, dev))
     _raise(rc, "gg_silu_mul_backward")
     return dH
@@ -331,7 +334,7 @@ def pack8(X: torch.Tensor, X8: Optional[torch.Tensor] = None,
     codes, dev = (cols + BLOCK8 - 1) // BLOCK8, X.get_device()
     X8 = _new(X8, (rows, cols), _E4M3, X, stream)
     scale = _new(scale, (rows, codes), _E8M0, X, stream)
-    rc = lib().gg_pack8(X.data_ptr(), rows, cols, _used_ptr(offs, False),
+    rc = lib().gg_pack8(X.data_ptr(), rows, cols, _used_ptr(offs, False, dev),
                         _arg(X8, "X8", (rows, cols), _E4M3, dev),
                         _arg(scale, "scale", (rows, codes), _E8M0, dev), _status_ptr(status),
                         _stream_handle(stream, dev))
@@ -349,7 +352,7 @@ def unpack8(X8: torch.Tensor, scale: torch.Tensor, X: Optional[torch.Tensor] = N
     X = _new(X, (rows, cols), _BF16, X8, stream)
     rc = lib().gg_unpack8(
         X8.data_ptr(), _arg(scale, "scale", (rows, (cols + BLOCK8 - 1) // BLOCK8), _E8M0, dev),
-        rows, cols, _used_ptr(offs, zero_tail), FLAG_ZERO_TAIL if zero_tail else 0,
+        rows, cols, _used_ptr(offs, zero_tail, dev), FLAG_ZERO_TAIL if zero_tail else 0,
         _arg(X, "X", (rows, cols), _BF16, dev), _status_ptr(status), _stream_handle(stream, dev))
     _raise(rc, "gg_unpack8")
     return X
