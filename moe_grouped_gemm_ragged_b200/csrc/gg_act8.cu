@@ -77,9 +77,9 @@ __device__ __forceinline__ bool leader() {
   return threadIdx.x % (G * W) == 0;
 }
 
-// Packed row of item b (an assignment, or a row), -1 for a dropped assignment; *live: the row
-// is in use. A row that may not be in use can be loaded from, as it is allocated, while *used
-// is still on its way.
+// Packed row of item b (an assignment, or a row), -1 for a dropped assignment. Without row_of the
+// row may not be in use; as it is allocated, it can be loaded from while *used is still on its
+// way, and what was loaded is then left.
 __device__ __forceinline__ int64_t row_of_item(const Params& p, int64_t b, int64_t used,
                                                bool report) {
   if (p.row_of == nullptr) return b;

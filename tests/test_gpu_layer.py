@@ -515,6 +515,29 @@ def test_silu_mul_by_assignment(T, k, E, N, concat):
     assert int(st.item()) == gg.DEV_BAD_ROUTE
 
 
+def test_rows8_and_silu_mul_past_32_bit_offsets():
+    """The last rows of an H of more than 2^31 elements."""
+    rows, N = 270000, 8192
+    H = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    H[rows - 2:] = torch.randn(2, N, device="cuda").to(torch.bfloat16)
+    want8 = ol.pack8_halves(to_f64(H[rows - 2:]), False)
+    H8 = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device="cuda")
+    s8 = torch.empty(rows, N // 32, dtype=torch.float8_e8m0fnu, device="cuda")
+    row_of = torch.tensor([rows - 1, rows - 2], dtype=torch.int32, device="cuda")
+    act = gg.silu_mul(H, row_of=row_of, H8=H8, H8_scale=s8)
+    small = gg.silu_mul(H[rows - 2:].clone())
+    assert torch.equal(act[rows - 2:], small)
+    dH = gg.silu_mul_backward(act, H8=H8, H8_scale=s8, row_of=row_of)
+    assert torch.equal(dH[rows - 2:], gg.silu_mul_backward(
+        small, H8=H8[rows - 2:].clone(), H8_scale=s8[rows - 2:].clone()))
+    del act, dH
+    H[:rows - 2] = 0
+    gg.pack8(H, H8, s8)
+    gg.unpack8(H8, s8, H)
+    np.testing.assert_array_equal(to_f64(H[rows - 2:]), want8)  # blocks of 32 either way
+    assert bool((H[:rows - 2:4999] == 0).all())
+
+
 def test_silu_mul_of_no_assignment():
     """An empty row_of names no row, whatever the rows in use are; the tail is cleared all the
     same."""
@@ -855,6 +878,58 @@ def test_captured_layer_step_replays_on_new_inputs():
             assert torch.equal(got[key].view(torch.uint8), t.view(torch.uint8)), (key, used)
         assert int(offs[-1]) == used * k
         assert bool((b["out"][used:].view(torch.int16) == 0).all())
+
+
+def test_captured_branches_that_fork_and_join():
+    """Calls on two branches of one capture, joined by a call that reads both, and two replays of
+    two such graphs at the same time."""
+    gen = torch.Generator(device="cuda").manual_seed(33)
+    T, k, N = 500, 2, 1024
+    x = torch.randn(T, 64, generator=gen, device="cuda")
+    Y = torch.randn(T * k, N, generator=gen, device="cuda").to(torch.bfloat16)
+    row_of = torch.randperm(T * k, generator=gen, device="cuda").to(torch.int32)
+
+    def make():
+        ids = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+        w, back = torch.zeros(T, k, device="cuda"), torch.zeros_like(Y)
+        x8 = torch.zeros(T * k, N, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        s8 = torch.zeros(T * k, N // 32, dtype=torch.uint8, device="cuda").view(
+            torch.float8_e8m0fnu)
+        out = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+        def step():
+            side.wait_stream(main)
+            gg.gate_topk(x, k, topk_ids=ids, weights=w, stream=main)
+            gg.pack8(Y, x8, s8, stream=side)
+            gg.unpack8(x8, s8, back, stream=side)
+            main.wait_stream(side)
+            gg.unroute(back, row_of, k, out, weights=w, stream=main)
+
+        torch.cuda.synchronize()
+        step()
+        torch.cuda.synchronize()
+        want = out.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            step()
+        for t in (w, back, out):
+            t.zero_()
+        torch.cuda.synchronize()
+        return graph, out, want
+
+    a, b = make(), make()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        for (graph, _, _), stream in zip((a, b), streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want in (a, b):
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    ids, w = gg.gate_topk(x, k)
+    x8, s8 = gg.pack8(Y)
+    assert torch.equal(a[2], gg.unroute(gg.unpack8(x8, s8), row_of, k, weights=w))
 
 
 def test_chain_of_calls_needs_no_synchronisation():
