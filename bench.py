@@ -41,11 +41,11 @@ UNIT = "TFLOP/s"
 # counters, which ncu collects in a single pass (nothing saved or restored); a launch list over
 # many kernels collects gpu__time_duration.sum alone.
 NCU_TRAFFIC = {
-    ("forward", "large"): 10.760e9,
-    ("dgrad", "large"): 12.944e9,
-    ("wgrad", "large"): 14.378e9,
+    ("forward", "large"): 11.899e9,
+    ("dgrad", "large"): 12.970e9,
+    ("wgrad", "large"): 16.147e9,
 }
-NCU_TRAFFIC_SRC_HASH = "a0da491e0ea04d57"
+NCU_TRAFFIC_SRC_HASH = "034efc478728fc44"
 
 
 GEMM_SOURCES = ("gg_kernel.cuh", "ptx.cuh", "gg_api.cu", "gg_masked.cuh")  # kernels + launch
