@@ -1,7 +1,8 @@
-"""Build step of the CUDA library: nvcc for sm_100a into ``libgg.so`` next to this file.
+"""Build step of the CUDA library: nvcc for sm_100a into ``libgg.so`` next to this file, and of
+the Python module ``_native`` (``csrc/binding.cpp``, the quick way into the layer's calls).
 
-Run ``python -m moe_grouped_gemm_ragged_b200._build`` (or call :func:`build`). The library
-is rebuilt when any source under ``csrc/`` or ``include/`` is newer than it.
+Run ``python -m moe_grouped_gemm_ragged_b200._build`` (or call :func:`build`). Each is rebuilt
+when a source of its own under ``csrc/`` or ``include/`` is newer than it.
 """
 from __future__ import annotations
 
@@ -9,12 +10,16 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgg.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+# for this interpreter only: another one does not find it and goes without
+NATIVE = os.path.join(PKG, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -52,8 +57,10 @@ def build(force: bool = False, verbose: bool = False, out: str = None, defines=(
     ``out`` and ``defines`` (``NAME=VALUE`` strings) build another copy with other tuning
     macros; such a copy is always rebuilt."""
     target = out or LIB
-    if out is None and not force and not stale():
-        return LIB
+    if out is None:
+        build_binding(force, verbose)
+        if not force and not stale():
+            return LIB
     tmp = target + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-I", CSRC,
            *sources(), "-o", tmp]
@@ -63,6 +70,31 @@ def build(force: bool = False, verbose: bool = False, out: str = None, defines=(
     subprocess.check_call(cmd)
     os.replace(tmp, target)
     return target
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile ``csrc/binding.cpp`` against this interpreter's torch unless it is up to date."""
+    inputs = [BINDING, os.path.join(INCLUDE, "gg.h")]
+    if (not force and os.path.exists(NATIVE)
+            and all(os.path.getmtime(f) <= os.path.getmtime(NATIVE) for f in inputs)):
+        return NATIVE
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in cpp_extension.include_paths()],
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-I", INCLUDE, BINDING, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 if __name__ == "__main__":

@@ -24,6 +24,11 @@ from torch.autograd.function import once_differentiable
 from . import (FLAG_GATE_UP_CONCAT, FLAG_ZERO_TAIL, _check, _raise, _status_ptr, _stream_handle,
                dgrad_ex, forward_ex, lib, route, wgrad_ex)
 
+try:  # csrc/binding.cpp: the calls below with their buffers in hand, 3 us sooner
+    from . import _native
+except ImportError:  # not built for this interpreter: the same through ctypes
+    _native = None
+
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 GATE_RENORM, GATE_LOGITS_F32 = 0x1, 0x2
 GATE_MAX_K = 32
@@ -48,6 +53,8 @@ def declare(L: ctypes.CDLL) -> None:
     }.items():
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
+        if _native is not None:
+            _native.bind(name, ctypes.cast(fn, P).value)
 
 
 def _on(stream):
@@ -128,6 +135,12 @@ def gate_topk(logits: torch.Tensor, k: int, *, score: int = GATE_SOFTMAX, renorm
     (GATE_SIGMOID only) is added to the scores for the choice alone. Logits of -inf are masked;
     a token with fewer than k others gets ids -1, which ``route`` drops, and weights 0 in its
     last slots. ``num_tokens`` int32 [1]: tokens in use of a padded batch, read on the device."""
+    if _native is not None:
+        rc = _native.gate_topk(logits, k, score, renorm, scale, bias, num_tokens, topk_ids,
+                               weights, status, stream)
+        if rc is not None:
+            _raise(rc, "gg_gate_topk")
+            return topk_ids, weights
     T, E, k, score, flags, scale, dev = _gate_args(logits, k, score, renorm, scale)
     if k < 1:
         raise ValueError("k must be positive")
@@ -147,6 +160,12 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
                        status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the logits (in their type, written in full) from that of the weights;
     ``topk_ids`` is what ``gate_topk`` returned for the same score, renorm and scale."""
+    if _native is not None:
+        rc = _native.gate_topk_backward(logits, topk_ids, dweights, dlogits, score, renorm, scale,
+                                        status, stream)
+        if rc is not None:
+            _raise(rc, "gg_gate_topk_backward")
+            return dlogits
     _check(topk_ids, "topk_ids", _I32, 2)
     T, E, k, score, flags, scale, dev = _gate_args(logits, topk_ids.shape[1], score, renorm,
                                                    scale)
@@ -181,6 +200,11 @@ def unroute(Y: torch.Tensor, row_of: torch.Tensor, k: int, out: Optional[torch.T
 
     Y bf16 [rows, N]; row_of int32 [T*k] from ``route`` (-1 adds nothing); weights float32 [T, k]
     (None: 1); residual bf16 [T, N] (None: 0; may be ``out``); out bf16 [T, N]."""
+    if _native is not None:
+        rc = _native.unroute(Y, row_of, k, out, weights, residual, status, stream)
+        if rc is not None:
+            _raise(rc, "gg_unroute")
+            return out
     _check(Y, "Y", _BF16, 2)
     dev = Y.get_device()
     T, k, rp = _tokens(row_of, k, dev)
@@ -205,6 +229,12 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
     (needs Y). Rows of dY that row_of does not name are left as they are; with ``zero_tail``
     those past the last of ``offs`` become zeros. row_of's rows must be distinct. Returns
     (dY, dweights)."""
+    if _native is not None:
+        rc = _native.unroute_backward(dout, row_of, k, dY, Y, weights, dweights, offs, zero_tail,
+                                      status, stream)
+        if rc is not None:
+            _raise(rc, "gg_unroute_backward")
+            return dY, dweights
     _check(dout, "dout", _BF16, 2)
     dev = dout.get_device()
     T, k, rp = _tokens(row_of, k, dev)
@@ -215,7 +245,9 @@ def unroute_backward(dout: torch.Tensor, row_of: torch.Tensor, k: int,
         raise ValueError("one of dY and dweights must be given")
     if dweights is not None and Y is None:
         raise ValueError("dweights needs Y")
-    rows = (dY if dY is not None else Y).shape[0]
+    packed, name = (dY, "dY") if dY is not None else (Y, "Y")
+    _check(packed, name, _BF16, 2)
+    rows = packed.shape[0]
     rc = lib().gg_unroute_backward(
         dout.data_ptr(), _arg(Y, "Y", (rows, N), _BF16, dev), rows, rp,
         _arg(weights, "weights", (T, k), _F32, dev), T, k, N, _used_ptr(offs, zero_tail, dev),
@@ -278,6 +310,12 @@ def silu_mul(H: torch.Tensor, act: Optional[torch.Tensor] = None, *,
     from ``route``, the rows that it names, with weights[i] of assignment i (any shape). With
     ``H8`` float8_e4m3fn [rows, N] and ``H8_scale`` float8_e8m0fnu [rows, 2*ceil(N/64)] the rows
     of H are also kept there in 8 bits, for ``silu_mul_backward``."""
+    if _native is not None:
+        rc = _native.silu_mul(H, act, offs, row_of, weights, gate_up_concat, zero_tail, H8,
+                              H8_scale, status, stream)
+        if rc is not None:
+            _raise(rc, "gg_silu_mul")
+            return act
     _check(H, "H", _BF16, 2)
     rows, N = H.shape
     dev = H.get_device()
@@ -305,6 +343,12 @@ def silu_mul_backward(dact: torch.Tensor, dH: Optional[torch.Tensor] = None, *,
     H8_scale or H. ``act`` (bf16 [rows, N/2]) is computed again into the given buffer, and the
     weights' gradient into ``dweights`` (float32, indexed like the weights; 0 for a dropped
     assignment)."""
+    if _native is not None:
+        rc = _native.silu_mul_backward(dact, dH, H, H8, H8_scale, offs, row_of, weights, act,
+                                       dweights, gate_up_concat, zero_tail, status, stream)
+        if rc is not None:
+            _raise(rc, "gg_silu_mul_backward")
+            return dH
     _check(dact, "dact", _BF16, 2)
     rows, half = dact.shape
     N, dev = 2 * half, dact.get_device()
@@ -329,6 +373,11 @@ def pack8(X: torch.Tensor, X8: Optional[torch.Tensor] = None,
     """The rows of X bf16 [rows, cols] in 8 bits: (X8 float8_e4m3fn [rows, cols], scale
     float8_e8m0fnu [rows, ceil(cols/32)]), X ~ X8 * scale with one power of two for 32 columns.
     Rows at and past the last of ``offs`` are not touched."""
+    if _native is not None:
+        rc = _native.pack8(X, X8, scale, offs, status, stream)
+        if rc is not None:
+            _raise(rc, "gg_pack8")
+            return X8, scale
     _check(X, "X", _BF16, 2)
     rows, cols = X.shape
     codes, dev = (cols + BLOCK8 - 1) // BLOCK8, X.get_device()
@@ -346,6 +395,11 @@ def unpack8(X8: torch.Tensor, scale: torch.Tensor, X: Optional[torch.Tensor] = N
             offs: Optional[torch.Tensor] = None, zero_tail: bool = False,
             status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """X bf16 [rows, cols] = X8 * scale, exact for what ``pack8`` wrote."""
+    if _native is not None:
+        rc = _native.unpack8(X8, scale, X, offs, zero_tail, status, stream)
+        if rc is not None:
+            _raise(rc, "gg_unpack8")
+            return X
     _check(X8, "X8", _E4M3, 2)
     rows, cols = X8.shape
     dev = X8.get_device()

@@ -1029,3 +1029,98 @@ def test_binding_refuses_shapes_strides_and_missing_arguments():
         gg.unroute(Y.view(-1)[1:1 + 4 * 256].view(4, 256), row_of[:4], 2)  # not on 16 bytes
     with pytest.raises(gg.GGError, match="UNSUPPORTED"):
         gg.silu_mul(Y[:, :128].contiguous())
+
+
+def _calls(T=6, k=2, E=16, N=512):
+    """Every call with all of its buffers: (function, positional, keywords)."""
+    def t(*shape, dtype=torch.bfloat16):
+        if dtype in (torch.bfloat16, torch.float32):
+            gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+            return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+        if dtype is torch.int32:
+            return torch.zeros(shape, dtype=dtype, device="cuda")
+        return torch.zeros(shape, dtype=torch.uint8, device="cuda").view(dtype)
+
+    f32, i32, e4, e8 = torch.float32, torch.int32, torch.float8_e4m3fn, torch.float8_e8m0fnu
+    n = T * k
+    row_of = torch.arange(n, dtype=i32, device="cuda")
+    num = torch.tensor([T], dtype=i32, device="cuda")
+    offs = torch.tensor([3, n], dtype=i32, device="cuda")
+    st = t(1, dtype=i32)
+    ids = torch.tensor([[1, 0]] * T, dtype=i32, device="cuda")
+    by = dict(offs=offs, row_of=row_of, weights=t(T, k, dtype=f32), status=st)
+    return [
+        (gg.gate_topk, [t(T, E, dtype=f32), k],
+         dict(score=gg.GATE_SIGMOID, bias=t(E, dtype=f32), num_tokens=num,
+              topk_ids=t(T, k, dtype=i32), weights=t(T, k, dtype=f32), status=st)),
+        (gg.gate_topk, [t(T, E), k], dict(topk_ids=t(T, k, dtype=i32),
+                                          weights=t(T, k, dtype=f32))),
+        (gg.gate_topk_backward, [t(T, E, dtype=f32), ids, t(T, k, dtype=f32),
+                                 t(T, E, dtype=f32)], dict(status=st)),
+        (gg.unroute, [t(n, N), row_of, k, t(T, N)],
+         dict(weights=t(T, k, dtype=f32), residual=t(T, N), status=st)),
+        (gg.unroute_backward, [t(T, N), row_of, k, t(n, N)],
+         dict(Y=t(n, N), weights=t(T, k, dtype=f32), dweights=t(T, k, dtype=f32), offs=offs,
+              zero_tail=True, status=st)),
+        (gg.silu_mul, [t(n, N), t(n, N // 2)],
+         dict(H8=t(n, N, dtype=e4), H8_scale=t(n, N // 32, dtype=e8), zero_tail=True, **by)),
+        (gg.silu_mul, [t(n, N), t(n, N // 2)], dict(weights=t(n, dtype=f32),
+                                                    gate_up_concat=True)),
+        (gg.silu_mul_backward, [t(n, N // 2), t(n, N)],
+         dict(H8=t(n, N, dtype=e4), H8_scale=t(n, N // 32, dtype=e8), act=t(n, N // 2),
+              dweights=t(T, k, dtype=f32), **by)),
+        (gg.silu_mul_backward, [t(n, N // 2), t(n, N)], dict(H=t(n, N), gate_up_concat=True)),
+        (gg.pack8, [t(n, N), t(n, N, dtype=e4), t(n, N // 32, dtype=e8)],
+         dict(offs=offs, status=st)),
+        (gg.unpack8, [t(n, N, dtype=e4), t(n, N // 32, dtype=e8), t(n, N)],
+         dict(offs=offs, zero_tail=True, status=st)),
+    ]
+
+
+def _tensors(fn, args, kw):
+    """What a call was given and has written, as bytes."""
+    fn(*args, **kw)
+    return [t.clone().view(torch.uint8) for t in [*args, *kw.values()]
+            if isinstance(t, torch.Tensor)]
+
+
+def test_calls_without_the_native_module(monkeypatch):
+    """The quick way into a call and the one through ctypes do the same."""
+    from moe_grouped_gemm_ragged_b200 import _layer
+    assert _layer._native is not None
+    quick = [_tensors(*c) for c in _calls()]
+    monkeypatch.setattr(_layer, "_native", None)
+    for a, b in zip(quick, [_tensors(*c) for c in _calls()]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("call", range(11))
+def test_every_tensor_argument_is_checked(call, native, monkeypatch):
+    """Another type, one row more, strides, the host, a list in its place: each refused with a
+    Python error, by either way into the call."""
+    from moe_grouped_gemm_ragged_b200 import _layer
+    if not native:
+        monkeypatch.setattr(_layer, "_native", None)
+    fn, args, kw = _calls()[call]
+    names = [i for i, a in enumerate(args) if isinstance(a, torch.Tensor)]
+    names += [key for key, a in kw.items() if isinstance(a, torch.Tensor)]
+    for name in names:
+        good = args[name] if isinstance(name, int) else kw[name]
+        raw = good.view(torch.uint8) if good.element_size() == 1 else good
+        longer = torch.cat([raw, raw[:1]]).view(good.dtype)
+        bad = [raw.double(), good.cpu(), raw.tolist()]
+        if name not in ("offs", "status") and not (fn is gg.unroute and name == 0):
+            bad.append(longer)  # those are of any length
+        if not (name in ("weights", "dweights") and fn in (gg.silu_mul, gg.silu_mul_backward)):
+            bad.append(good[None])  # those are of any shape
+        if good.numel() > 1 and good.element_size() > 1:
+            bad.append(torch.stack([good, good], -1).select(-1, 0))
+        for b in bad:
+            a2, k2 = list(args), dict(kw)
+            if isinstance(name, int):
+                a2[name] = b
+            else:
+                k2[name] = b
+            with pytest.raises((ValueError, TypeError)):
+                fn(*a2, **k2)

@@ -223,3 +223,23 @@ def test_binding_refuses_host_tensors_and_types():
                  lambda: gg.unpack8(torch.zeros(4, 32, dtype=torch.float8_e4m3fn), bf)):
         with pytest.raises(ValueError, match="must be a CUDA tensor"):
             call()
+
+
+def test_native_module_takes_only_what_it_can_check(lib):
+    """Anything but device tensors (and too few arguments, or none bound) is left to the Python
+    checks: None, and no error set."""
+    from moe_grouped_gemm_ragged_b200 import _layer
+    n = _layer._native
+    assert n is not None, "csrc/binding.cpp has not been built for this interpreter"
+    bf, i32 = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    assert n.unroute(bf, i32, 1, bf, None, None, None, None) is None
+    assert n.unroute(bf) is None and n.pack8() is None
+    assert n.gate_topk(bf, 2, 0, True, 1.0, None, None, None, None, None, None) is None
+    assert n.gate_topk("x", None, 0, 1, 1, None, None, None, None, None, None) is None
+    assert n.silu_mul(None, *[None] * 10) is None
+    with pytest.raises(ValueError):
+        n.bind("gg_forward", 1)
+    with pytest.raises(ValueError):
+        n.bind("gg_unroute")
+    with pytest.raises(TypeError):
+        n.bind("gg_unroute", "1")
