@@ -166,6 +166,14 @@ __device__ __forceinline__ float sigmoid_over(float x, float m) {
   return __fdividef(expf(fminf(x, 0.f) - m), 1.f + expf(-fabsf(x)));
 }
 
+// e^x for x <= 0 by the hardware's power: off by 2 + |x| / 2 units of 2^-23, which a sum of a
+// token's exponentials, the large ones of which have small |x|, hardly shows. 0 of -inf.
+__device__ __forceinline__ float fast_exp(float x) {
+  float t = x * 1.44269504f;
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t));
+  return t;
+}
+
 // The score that a biased choice tries first. In units of 2^-23 it is off by at most
 // sigma (1 - sigma) (2 + 1.17 |x|) < 0.6 from the fast exponential, 2.5 from the sum and the
 // reciprocal and (1 + |bias|) / 2 from the last sum; two scores further apart than CLOSE
@@ -224,10 +232,10 @@ __device__ __forceinline__ uint32_t packed(float v, int expert) {
 }
 __device__ __forceinline__ int expert_of(uint32_t key) { return (int)(NUMBER - (key & NUMBER)); }
 
-// The `want` largest keys of the group, in order, into c.id. Each lane sorts its keys once; a
-// round compares only the lanes' first keys and moves the winner's up. Returns how many there
-// are.
-template <int G, int NV, typename C>
+// The `want` largest keys of the group, in order, into c.id. Each lane has sorted its keys; a
+// round compares only the lanes' first keys and moves the winner's up, of which only DEPTH (at
+// least `want`, or all of them) can still come first. Returns how many there are.
+template <int G, int DEPTH, int NV, typename C>
 __device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_t (&key)[NV],
                                       C& c) {
   for (int s = 0; s < want; ++s) {
@@ -235,8 +243,8 @@ __device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_
     if (top < LOWEST) return s;  // nothing left
     const bool won = key[0] == top;
 #pragma unroll
-    for (int j = 0; j + 1 < NV; ++j) key[j] = won ? key[j + 1] : key[j];
-    key[NV - 1] = won ? 0u : key[NV - 1];
+    for (int j = 0; j + 1 < DEPTH; ++j) key[j] = won ? key[j + 1] : key[j];
+    key[DEPTH - 1] = won ? 0u : key[DEPTH - 1];
     if (lane == 0) c.id[s] = (int32_t)top;
   }
   return want;
@@ -431,7 +439,8 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       }
       sort_keys(key);
     }
-    got = choose<G, NV>(mask, lane, want, key, c);
+    if (NV > 8 && want <= 8) got = choose<G, 8>(mask, lane, want, key, c);
+    else got = choose<G, NV>(mask, lane, want, key, c);
     __syncwarp(mask);
 #pragma unroll 1
     for (int s = lane; s < got; s += G) {
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       }
     } else if constexpr (!BIAS) {  // a biased gate is a sigmoid
 #pragma unroll
-      for (int j = 0; j < NV; ++j) total += expf(x[j] - m);  // 0 of -inf
+      for (int j = 0; j < NV; ++j) total += fast_exp(x[j] - m);
     }
     total = group_sum<G>(mask, total);
   }
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
     top = fmaxf(group_max<G>(mask, top), -FLT_MAX);  // all of them masked: every share is 0
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      x[j] = expf(x[j] - top);
+      x[j] = fast_exp(x[j] - top);
       total += x[j];
       mean = fmaf(x[j], out[j], mean);
     }
