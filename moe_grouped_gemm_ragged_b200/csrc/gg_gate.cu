@@ -177,8 +177,7 @@ __device__ __forceinline__ float fast_exp(float x) {
 // The score that a biased choice tries first. In units of 2^-23 it is off by at most
 // sigma (1 - sigma) (2 + 1.17 |x|) < 0.6 from the fast exponential, 2.5 from the sum and the
 // reciprocal and (1 + |bias|) / 2 from the last sum; two scores further apart than CLOSE
-// (1 + |bias| + |bias'|) are in the right order, with half of CLOSE to spare. (3 in place
-// of 1 where one of the two biases is not known.)
+// (1 + |bias| + |bias'|) are in the right order, with half of CLOSE to spare.
 __device__ __forceinline__ float fast_score(float x, float b) {
   float t = x * -1.44269504f;  // 1 / (1 + 2^(-x log2 e))
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t));
@@ -188,11 +187,11 @@ __device__ __forceinline__ float fast_score(float x, float b) {
 }
 constexpr float CLOSE = 16.f / 8388608.f;
 
-// The order is looked up this many places further than needed, to see that no other expert may
-// belong to the chosen. Scores under a bias lie closer: with two places about one token in ten
-// thousand of 256 experts stays open, and one such token adds 4 us to a call.
-template <bool BIAS>
-constexpr int MORE = BIAS ? 3 : 2;
+// fp32 orders are looked up past the k-th until it is seen that no other expert may belong to
+// the chosen, one place most often and this many at most. (With a fixed two places about one
+// biased token in ten thousand of 256 experts stayed open, and one such token adds 4 us to a
+// call.)
+constexpr int MORE = 4;
 
 template <int SLOTS>
 struct Chosen {  // of one token, in shared memory
@@ -232,13 +231,25 @@ __device__ __forceinline__ uint32_t packed(float v, int expert) {
 }
 __device__ __forceinline__ int expert_of(uint32_t key) { return (int)(NUMBER - (key & NUMBER)); }
 
-// The `want` largest keys of the group, in order, into c.id. Each lane has sorted its keys; a
-// round compares only the lanes' first keys and moves the winner's up, of which only DEPTH (at
-// least `want`, or all of them) can still come first. Returns how many there are.
-template <int G, int DEPTH, int NV, typename C>
-__device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_t (&key)[NV],
-                                      C& c) {
-  for (int s = 0; s < want; ++s) {
+// Whether what has the key b, or one below it, is surely under the first k, which have the key a
+// or one above it. Under a bias |bias| <= |score| + 1 for the scores' errors.
+template <bool BIAS>
+__device__ __forceinline__ bool apart(uint32_t a, uint32_t b) {
+  if constexpr (!BIAS) return (a ^ b) > NUMBER;
+  const float va = value_of(a & ~NUMBER), vb = value_of(b | NUMBER);
+  return va - vb > CLOSE * (3.f + fabsf(va) + fabsf(vb) + 2.f);
+}
+
+// The k largest keys of the group, in order, into c.id, and with ORDER more until the k-th is
+// apart from the last, `most` at most (*open: it is not, and there are others). Each lane has
+// sorted its keys; a round compares only the lanes' first keys and moves the winner's up, of
+// which only DEPTH (at least `most`, or all of them) can still come first. Returns how many.
+enum class Order { WHOLE, LOGITS, SCORES };
+template <int G, int DEPTH, Order ORDER, int NV, typename C>
+__device__ __forceinline__ int choose(uint32_t mask, int lane, int k, int most,
+                                      uint32_t (&key)[NV], C& c, bool* open) {
+  uint32_t kth = 0;
+  for (int s = 0; s < most; ++s) {
     const uint32_t top = group_max<G>(mask, key[0]);
     if (top < LOWEST) return s;  // nothing left
     const bool won = key[0] == top;
@@ -246,8 +257,15 @@ __device__ __forceinline__ int choose(uint32_t mask, int lane, int want, uint32_
     for (int j = 0; j + 1 < DEPTH; ++j) key[j] = won ? key[j + 1] : key[j];
     key[DEPTH - 1] = won ? 0u : key[DEPTH - 1];
     if (lane == 0) c.id[s] = (int32_t)top;
+    if constexpr (ORDER != Order::WHOLE) {
+      if (s >= k - 1) {
+        if (s == k - 1) kth = top;
+        else if (apart<ORDER == Order::SCORES>(kth, top)) return s + 1;
+      }
+    }
   }
-  return want;
+  *open = ORDER != Order::WHOLE;
+  return most;
 }
 
 // What decides the order: sigma(x) + b under a bias, else x.
@@ -398,7 +416,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
                                                        bool wide, bool wide_bias) {
   after_previous();
   constexpr bool EXACT = !BIAS && sizeof(L) == 2;  // the keys hold the whole value
-  constexpr int SLOTS = GG_GATE_MAX_K + (EXACT ? 0 : MORE<BIAS>);
+  constexpr int SLOTS = GG_GATE_MAX_K + (EXACT ? 0 : MORE);
   __shared__ Chosen<SLOTS> chosen[THREADS / G];
   __shared__ double doubles[EXACT ? 1 : THREADS / G][EXACT ? 1 : SLOTS];
   const int lane = threadIdx.x % G;
@@ -417,7 +435,8 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
   int got = 0;
   if (t < live_tokens) {
     uint32_t key[NV];
-    const int want = EXACT ? p.k : min(p.k + MORE<BIAS>, p.E);
+    const int most = EXACT ? p.k : min(p.k + MORE, p.E);
+    bool open = false;
     if constexpr (EXACT) {
       bf16_keys<NV>(mask, lane * NV, row, p.E, wide, key, x, &bad);
     } else {
@@ -439,8 +458,10 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       }
       sort_keys(key);
     }
-    if (NV > 8 && want <= 8) got = choose<G, 8>(mask, lane, want, key, c);
-    else got = choose<G, NV>(mask, lane, want, key, c);
+    constexpr Order ORDER = EXACT ? Order::WHOLE : BIAS ? Order::SCORES : Order::LOGITS;
+    if (NV > 8 && most <= 8) got = choose<G, 8, ORDER>(mask, lane, p.k, most, key, c, &open);
+    else got = choose<G, NV, ORDER>(mask, lane, p.k, most, key, c, &open);
+    open = open && most < p.E;  // the same for the group
     __syncwarp(mask);
 #pragma unroll 1
     for (int s = lane; s < got; s += G) {
@@ -454,34 +475,19 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
     }
     if constexpr (!EXACT) {
       __syncwarp(mask);
-      bool close = false, open = false;
+      bool close = false;
 #pragma unroll 1
-      for (int s = lane; s < got; s += G) {
-        const bool kth = s == p.k - 1 && got == want && want < p.E;
+      for (int s = lane; s + 1 < got; s += G) {
+        const float x0 = c.x[s], x1 = c.x[s + 1];
         if constexpr (BIAS) {
-          const float ba = p.bias[c.id[s]];
-          if (s + 1 < got) {
-            const float bb = p.bias[c.id[s + 1]];
-            close |= c.score[s] - c.score[s + 1] <= CLOSE * (1.f + fabsf(ba) + fabsf(bb)) &&
-                     !(c.x[s] == c.x[s + 1] && ba == bb);
-          }
-          if (kth) {
-            const float bb = p.bias[c.id[got - 1]];
-            // the first k are at least at the k-th's 22 bits, what follows at most at the last's
-            open = value_of(key_of(c.score[s]) & ~NUMBER) -
-                       value_of(key_of(c.score[got - 1]) | NUMBER) <=
-                   CLOSE * (3.f + fabsf(ba) + fabsf(bb));
-          }
+          const float b0 = p.bias[c.id[s]], b1 = p.bias[c.id[s + 1]];
+          close |= c.score[s] - c.score[s + 1] <= CLOSE * (1.f + fabsf(b0) + fabsf(b1)) &&
+                   !(x0 == x1 && b0 == b1);
         } else {
-          const float x0 = c.x[s];
-          if (s + 1 < got) {
-            const float x1 = c.x[s + 1];
-            close |= !(x0 > x1 || (x0 == x1 && c.id[s] < c.id[s + 1]));
-          }
-          if (kth) open = (key_of(x0) ^ key_of(c.x[got - 1])) <= NUMBER;
+          close |= !(x0 > x1 || (x0 == x1 && c.id[s] < c.id[s + 1]));
         }
       }
-      if (__any_sync(mask, open)) {
+      if (open) {
         got = choose_double<L, G, NV, BIAS>(mask, lane, p.k, row, p.bias, p.E, c.id);
         __syncwarp(mask);
         for (int s = lane; s < got; s += G) c.x[s] = to_float(row[c.id[s]]);
