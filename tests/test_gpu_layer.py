@@ -741,6 +741,22 @@ def test_gate_gradient_of_an_only_expert_is_zero(score, dtype):
         assert bool((dx == 0).all())
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_gate_gradient_of_gains_that_hardly_differ(sigmoid):
+    """Renormalised weights whose gradients differ in their last bits: dx_i = v_i (g_i - sum g v),
+    the differences of the g in full (the first is taken off, exactly where they are so close)."""
+    gen = torch.Generator().manual_seed(6)
+    x = torch.randn(200, 32, generator=gen)
+    dw = 1.0 + 2.0 ** -20 * torch.randint(-8, 9, (200, 4), generator=gen)
+    score = gg.GATE_SIGMOID if sigmoid else gg.GATE_SOFTMAX
+    ids, _ = gg.gate_topk(x.cuda(), 4, score=score)
+    dx = gg.gate_topk_backward(x.cuda(), ids, dw.cuda(), score=score)
+    ref = ol.gate_backward(x.double().numpy(), ids.cpu().numpy(), (dw.double() - 1).numpy(),
+                           sigmoid)
+    # |g| up to 2^-17; a few dozen roundings of products of that size
+    _near(dx.cpu().double().numpy(), ref, 64 * U * 2.0 ** -16 + F32_TINY, "dlogits")
+
+
 def test_gate_gradient_of_an_expert_named_twice():
     """ids that gate_topk would not make: both slots add to their expert, in order."""
     x = torch.randn(3, 40, generator=torch.Generator().manual_seed(8))
