@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
   for (int j = 0; j < NV / 4; ++j)
     *reinterpret_cast<float4*>(d + (j * G + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false;
-  float m = -INFINITY, g0 = 0.f;
+  float m = -INFINITY;
 #pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
     int32_t id = p.ids[t * p.k + s];
@@ -594,14 +594,10 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
     }
     c.id[s] = id;
     c.g[s] = g;
-    if (s == lane) g0 = g;
   }
   if (!full) {
     float mean = 0.f;
     if (renorm) {
-      // the first slot's g is taken off all of them (g - sum g v stays the same), so that gains
-      // that hardly differ lose nothing
-      g0 = __shfl_sync(mask, g0, 0, G);
       m = group_max<G>(mask, m);
       float total = 0.f;
 #pragma unroll 1
@@ -615,10 +611,20 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
       for (int s = lane; s < p.k; s += G) {
         if (c.id[s] < 0) continue;
         c.v[s] /= total;  // a true quotient: the share of an only slot is 1 and its gradient 0
-        c.g[s] -= g0;
         mean = fmaf(c.g[s], c.v[s], mean);
       }
       mean = group_sum<G>(mask, mean);
+      // The mean of what is left takes the first mean's rounding off: gains that hardly differ
+      // keep their differences, whatever the shares.
+      float rest = 0.f;
+#pragma unroll 1
+      for (int s = lane; s < p.k; s += G) {
+        if (c.id[s] < 0) continue;
+        c.g[s] -= mean;
+        rest = fmaf(c.g[s], c.v[s], rest);
+      }
+      rest = group_sum<G>(mask, rest);
+      mean = rest == rest ? rest : 0.f;  // an infinite gain: the plain formula's values
     }
 #pragma unroll 1
     for (int s = lane; s < p.k; s += G) {

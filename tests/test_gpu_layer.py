@@ -744,7 +744,7 @@ def test_gate_gradient_of_an_only_expert_is_zero(score, dtype):
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_gate_gradient_of_gains_that_hardly_differ(sigmoid):
     """Renormalised weights whose gradients differ in their last bits: dx_i = v_i (g_i - sum g v),
-    the differences of the g in full (the first is taken off, exactly where they are so close)."""
+    the differences of the g in full."""
     gen = torch.Generator().manual_seed(6)
     x = torch.randn(200, 32, generator=gen)
     dw = 1.0 + 2.0 ** -20 * torch.randint(-8, 9, (200, 4), generator=gen)
@@ -755,6 +755,31 @@ def test_gate_gradient_of_gains_that_hardly_differ(sigmoid):
                            sigmoid)
     # |g| up to 2^-17; a few dozen roundings of products of that size
     _near(dx.cpu().double().numpy(), ref, 64 * U * 2.0 ** -16 + F32_TINY, "dlogits")
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_gate_gradient_with_a_large_gain_of_a_small_share(sigmoid):
+    """A first slot of next to no share (a balancing bias can make one) and a large gain takes
+    nothing from the others' gradients; a slot whose logit is masked counts for nothing at all."""
+    gen = torch.Generator().manual_seed(7)
+    T, E, k = 100, 16, 5
+    x = torch.randn(T, E, generator=gen)
+    ids = torch.arange(k, dtype=torch.int32).repeat(T, 1)
+    dw = torch.randn(T, k, generator=gen)
+    x[:, 0], dw[:, 0] = -25.0, 1e8
+    x[50:, 2], dw[50:, 2] = -float("inf"), float("inf")
+    score = gg.GATE_SIGMOID if sigmoid else gg.GATE_SOFTMAX
+    dx = gg.gate_topk_backward(x.cuda(), ids.cuda(), dw.cuda(), score=score)
+    live = np.where(np.isfinite(dw.numpy()), dw.double().numpy(), 0.0)
+    ref = ol.gate_backward(x.double().numpy(), ids.numpy(), live, sigmoid)
+    v = np.where(np.isfinite(x.numpy()), x.double().numpy(), -700.0)[:, :k]
+    v = 1 / (1 + np.exp(-v)) if sigmoid else np.exp(v)
+    v /= v.sum(1, keepdims=True)
+    # each share is off by a few roundings and its exponent's, 25 U; the mean by those of its terms
+    mean = (v * np.abs(live)).sum(1, keepdims=True)
+    bound = np.full((T, E), F32_TINY)
+    bound[:, :k] += 64 * U * v * (np.abs(live) + mean)
+    _near(dx.cpu().double().numpy(), ref, bound, "dlogits")
 
 
 def test_gate_gradient_of_an_expert_named_twice():
