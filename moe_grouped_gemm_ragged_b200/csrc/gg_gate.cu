@@ -140,7 +140,7 @@ __device__ __forceinline__ uint64_t group_max(uint32_t mask, uint64_t v) {
 // expert that cannot be chosen. + 0 turns -0 into +0: the two are a tie.
 __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
@@ -165,6 +165,13 @@ __device__ __forceinline__ float logit_or_mask(float x, bool* bad) {
 __device__ __forceinline__ float sigmoid_over(float x, float m) {
   return __fdividef(expf(fminf(x, 0.f) - m), 1.f + expf(-fabsf(x)));
 }
+__device__ __forceinline__ float sigmoid(float x) {
+  const float e = expf(-fabsf(x));
+  return __fdividef(x < 0.f ? e : 1.f, 1.f + e);
+}
+// Shares are taken of plain scores where their sum is above this: what a score below the normal
+// numbers loses is then under 2^-129 of the sum. Else of scores relative to the largest.
+constexpr float PLAIN = 0x1p-20f;
 
 // e^x for x <= 0 by the hardware's power: off by 2 + |x| / 2 units of 2^-23, which a sum of a
 // token's exponentials, the large ones of which have small |x|, hardly shows. 0 of -inf.
@@ -199,6 +206,7 @@ struct Chosen {  // of one token, in shared memory
   int32_t id[SLOTS];
   float x[SLOTS];
   float score[SLOTS];
+  float bias[SLOTS];
 };
 
 // Batcher's odd-even merge sort of a lane's keys, largest first.
@@ -228,6 +236,11 @@ constexpr uint32_t LOWEST = 0x00800000u;  // of the lowest finite number
 static_assert(GG_MAX_EXPERTS <= NUMBER + 1, "an expert's number fits the key");
 __device__ __forceinline__ uint32_t packed(float v, int expert) {
   return (key_of(v) & ~NUMBER) | (NUMBER - expert);
+}
+// A sum of a sigma is never -0.
+__device__ __forceinline__ uint32_t packed_score(float v, int expert) {
+  const uint32_t u = __float_as_uint(v);
+  return ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & ~NUMBER) | (NUMBER - expert);
 }
 __device__ __forceinline__ int expert_of(uint32_t key) { return (int)(NUMBER - (key & NUMBER)); }
 
@@ -441,17 +454,31 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       bf16_keys<NV>(mask, lane * NV, row, p.E, wide, key, x, &bad);
     } else {
       load_row<NV>(row, lane * NV, p.E, wide, x);
-      float b[NV];
-      if constexpr (BIAS) load_row<NV>(p.bias, lane * NV, p.E, wide_bias, b);
+      if constexpr (BIAS) {
+        float b[NV];
+        load_row<NV>(p.bias, lane * NV, p.E, wide_bias, b);
+        // a bias of -inf makes the score and so a key that cannot be chosen
+        bool odd = false;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        bool in = fabsf(x[j]) < INFINITY;
-        bad |= !(x[j] < INFINITY);
-        if constexpr (BIAS) {
-          bad |= in && !(b[j] < INFINITY);
-          in = in && fabsf(b[j]) < INFINITY;
-          key[j] = in ? packed(fast_score(x[j], b[j]), lane * NV + j) : 0u;
-        } else {
+        for (int j = 0; j < NV; ++j) {
+          odd |= !(x[j] < INFINITY);
+          const uint32_t u = packed_score(fast_score(x[j], b[j]), lane * NV + j);
+          key[j] = x[j] == -INFINITY ? 0u : u;
+          odd |= key[j] >= KEY_INF;
+        }
+        if (odd) {  // almost never
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const bool in = fabsf(x[j]) < INFINITY;
+            bad |= !(x[j] < INFINITY) || (in && !(b[j] < INFINITY));
+            if (!in || !(b[j] < INFINITY)) key[j] = 0;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const bool in = fabsf(x[j]) < INFINITY;
+          bad |= !(x[j] < INFINITY);
           key[j] = in ? packed(x[j], lane * NV + j) : 0u;
           x[j] = in ? x[j] : -INFINITY;
         }
@@ -471,7 +498,10 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       if constexpr (EXACT)  // the key's value again
         c.x[s] = value_of((k & 0xffff0000u) | ((k >> 31) ? 0u : 0xffffu));
       else c.x[s] = to_float(row[id]);
-      if constexpr (BIAS) c.score[s] = fast_score(c.x[s], p.bias[id]);
+      if constexpr (BIAS) {
+        c.bias[s] = p.bias[id];
+        c.score[s] = fast_score(c.x[s], c.bias[s]);
+      }
     }
     if constexpr (!EXACT) {
       __syncwarp(mask);
@@ -480,7 +510,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
       for (int s = lane; s + 1 < got; s += G) {
         const float x0 = c.x[s], x1 = c.x[s + 1];
         if constexpr (BIAS) {
-          const float b0 = p.bias[c.id[s]], b1 = p.bias[c.id[s + 1]];
+          const float b0 = c.bias[s], b1 = c.bias[s + 1];
           close |= c.score[s] - c.score[s + 1] <= CLOSE * (1.f + fabsf(b0) + fabsf(b1)) &&
                    !(x0 == x1 && b0 == b1);
         } else {
@@ -498,38 +528,40 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
     }
     __syncwarp(mask);
   }
+  // shares: each score over the sum of the chosen (renorm) or of all (softmax)
+  const bool sig = BIAS || sigmoid;  // a biased gate is a sigmoid
   float m = 0.f, total = 1.f;
-  if (got > 0 && (renorm || !sigmoid)) {
-    // shares: each score over the sum of the chosen (renorm) or of all (softmax), both relative
-    // to the largest; without a bias the first has it
-    m = c.x[0];
-    if constexpr (BIAS) {
+  if (got > 0 && (renorm || !sig)) {
+    if (!sig) m = c.x[0];  // the largest
+    for (bool again = false;; again = true) {
+      total = 0.f;
+      if (renorm) {
+#pragma unroll 1
+        for (int s = lane; s < got; s += G) {
+          float v;
+          if (sig) v = again ? sigmoid_over(c.x[s], m) : gate::sigmoid(c.x[s]);
+          else v = expf(c.x[s] - m);
+          c.score[s] = v;
+          total += v;
+        }
+      } else if constexpr (!BIAS) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) total += fast_exp(x[j] - m);
+      }
+      total = group_sum<G>(mask, total);
+      if (again || !sig || total >= PLAIN) break;
       m = -INFINITY;
 #pragma unroll 1
       for (int s = lane; s < got; s += G) m = fmaxf(m, c.x[s]);
-      m = group_max<G>(mask, m);
+      m = fminf(group_max<G>(mask, m), 0.f);
     }
-    if (sigmoid) m = fminf(m, 0.f);
-    total = 0.f;
-    if (renorm) {
-#pragma unroll 1
-      for (int s = lane; s < got; s += G) {
-        const float v = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
-        c.score[s] = v;
-        total += v;
-      }
-    } else if constexpr (!BIAS) {  // a biased gate is a sigmoid
-#pragma unroll
-      for (int j = 0; j < NV; ++j) total += fast_exp(x[j] - m);
-    }
-    total = group_sum<G>(mask, total);
   }
 #pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
     float w = 0.f;
     if (s < got) {
       if (renorm) w = c.score[s];
-      else w = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
+      else w = sig ? gate::sigmoid(c.x[s]) : expf(c.x[s] - m);
       w = p.scale * (w / total);  // a true quotient: the share of an only slot is 1
     }
     p.ids[t * p.k + s] = s < got ? c.id[s] : -1;
