@@ -34,6 +34,8 @@ struct Params {
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // NV neighbouring logits of a row (first: the lane's first expert, lane * NV); the rest of the
 // lane's share, past E, is masked. wide: E is a multiple of 8 and the rows start on 16 bytes, so
@@ -577,20 +579,17 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
 //   sigmoid               dx_i = g_i s_i (1 - s_i)
 //   sigmoid renormalised  dx_i = v_i (1 - s_i) (g_i - sum g v)
 // The scores are computed again from the logits; dx of a logit that was not chosen is 0 but for
-// the first form. A slot of id -1 carries nothing. A row in shared memory brings the slots to
-// their experts' lanes: it takes g (first form) or dx (the others); slots of the same expert
-// add up in their order. What bounds the kernel is the chain of these steps: a GPU full of tokens
-// is one wave.
+// the first form, which has a kernel of its own. A slot of id -1 carries nothing; slots of the
+// same expert (such ids do not come from gate_topk) add up in their order. What bounds both
+// kernels is the chain of their steps: a GPU full of tokens is one wave.
 struct Slots {  // of one token, in shared memory
   int32_t id[GG_GATE_MAX_K];
-  float x[GG_GATE_MAX_K];
-  float g[GG_GATE_MAX_K];  // scale * dweights, then dx
-  float v[GG_GATE_MAX_K];
+  float g[GG_GATE_MAX_K];
 };
 
+// Softmax over all experts. A row in shared memory brings the slots to their experts' lanes.
 template <typename L, int G, int NV>
-__global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool sigmoid,
-                                                                bool renorm, bool wide) {
+__global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool wide) {
   after_previous();
   __shared__ Slots slots[THREADS / G];
   // four experts of every lane side by side, then the next four: lanes' vectors are neighbours;
@@ -602,69 +601,20 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
   const uint32_t mask = group_mask<G>();
   Slots& c = slots[threadIdx.x / G];  // each lane reads only its own
   float* d = rows[threadIdx.x / G];
-  const L* row = static_cast<const L*>(p.logits) + t * p.E;
-  const bool full = !sigmoid && !renorm;
   float x[NV];
-  if (full) load_row<NV>(row, lane * NV, p.E, wide, x);
+  load_row<NV>(static_cast<const L*>(p.logits) + t * p.E, lane * NV, p.E, wide, x);
 #pragma unroll
   for (int j = 0; j < NV / 4; ++j)
     *reinterpret_cast<float4*>(d + (j * G + lane) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false;
-  float m = -INFINITY;
 #pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
     int32_t id = p.ids[t * p.k + s];
     float g = p.scale * p.dweights[t * p.k + s];
     bad |= id >= p.E;
     if (id < 0 || id >= p.E) id = -1, g = 0.f;
-    if (!full && id >= 0) {
-      bool ignored = false;
-      const float xs = logit_or_mask(to_float(row[id]), &ignored);
-      c.x[s] = xs;
-      if (xs > -INFINITY) m = fmaxf(m, sigmoid ? fminf(xs, 0.f) : xs);
-      else id = -1;
-    }
     c.id[s] = id;
     c.g[s] = g;
-  }
-  if (!full) {
-    float mean = 0.f;
-    if (renorm) {
-      m = group_max<G>(mask, m);
-      float total = 0.f;
-#pragma unroll 1
-      for (int s = lane; s < p.k; s += G) {
-        if (c.id[s] < 0) continue;
-        c.v[s] = sigmoid ? sigmoid_over(c.x[s], m) : expf(c.x[s] - m);
-        total += c.v[s];
-      }
-      total = group_sum<G>(mask, total);
-#pragma unroll 1
-      for (int s = lane; s < p.k; s += G) {
-        if (c.id[s] < 0) continue;
-        c.v[s] /= total;  // a true quotient: the share of an only slot is 1 and its gradient 0
-        mean = fmaf(c.g[s], c.v[s], mean);
-      }
-      mean = group_sum<G>(mask, mean);
-      // The mean of what is left takes the first mean's rounding off: gains that hardly differ
-      // keep their differences, whatever the shares.
-      float rest = 0.f;
-#pragma unroll 1
-      for (int s = lane; s < p.k; s += G) {
-        if (c.id[s] < 0) continue;
-        c.g[s] -= mean;
-        rest = fmaf(c.g[s], c.v[s], rest);
-      }
-      rest = group_sum<G>(mask, rest);
-      mean = rest == rest ? rest : 0.f;  // an infinite gain: the plain formula's values
-    }
-#pragma unroll 1
-    for (int s = lane; s < p.k; s += G) {
-      if (c.id[s] < 0) continue;
-      float v = renorm ? c.v[s] : sigmoid_over(c.x[s], 0.f);
-      if (sigmoid) v *= sigmoid_over(-c.x[s], 0.f);  // 1 - sigma(x) = sigma(-x)
-      c.g[s] = v * (c.g[s] - mean);
-    }
   }
   __syncwarp(mask);
   for (int s0 = 0; s0 < p.k; s0 += G) {
@@ -695,25 +645,95 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool s
     const float4 v = *reinterpret_cast<const float4*>(d + (j * G + lane) * 4);
     out[4 * j] = v.x, out[4 * j + 1] = v.y, out[4 * j + 2] = v.z, out[4 * j + 3] = v.w;
   }
-  if (full) {
-    bool ignored = false;
-    float top = -INFINITY, total = 0.f, mean = 0.f;
+  bool ignored = false;
+  float top = -INFINITY, total = 0.f, mean = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) top = fmaxf(top, x[j] = logit_or_mask(x[j], &ignored));
-    top = fmaxf(group_max<G>(mask, top), -FLT_MAX);  // all of them masked: every share is 0
+  for (int j = 0; j < NV; ++j) top = fmaxf(top, x[j] = logit_or_mask(x[j], &ignored));
+  top = fmaxf(group_max<G>(mask, top), -FLT_MAX);  // all of them masked: every share is 0
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      x[j] = fast_exp(x[j] - top);
-      total += x[j];
-      mean = fmaf(x[j], out[j], mean);
-    }
-    const float inv = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 1e-30f));
-    mean = group_sum<G>(mask, mean) * inv;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) out[j] = x[j] * inv * (out[j] - mean);
+  for (int j = 0; j < NV; ++j) {
+    x[j] = fast_exp(x[j] - top);
+    total += x[j];
+    mean = fmaf(x[j], out[j], mean);
   }
+  const float inv = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 1e-30f));
+  mean = group_sum<G>(mask, mean) * inv;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) out[j] = x[j] * inv * (out[j] - mean);
   store_row<NV>(static_cast<L*>(p.dlogits) + t * p.E, lane * NV, p.E, wide, out);
   if (bad) flag(p.status, GG_DEV_BAD_ROUTE);
+}
+
+// The other forms, a lane for each slot (k <= G): zeros first, so that they are on their way to
+// memory while the chosen are computed, then those over them. (16411 x 256 fp32, top 6, and
+// 131072 x 64 bf16, top 8: 5.0 and 14.4 us, 9.0 and 34 through a row in shared memory as above.)
+template <typename L, int G>
+__global__ void __launch_bounds__(THREADS) gate_backward_chosen_kernel(Params p, bool sig,
+                                                                       bool renorm, bool wide) {
+  after_previous();
+  const int lane = threadIdx.x % G;
+  const int64_t t = (int64_t)blockIdx.x * (THREADS / G) + threadIdx.x / G;
+  if (t >= p.T) return;  // the whole group
+  const uint32_t mask = group_mask<G>();
+  int32_t id = -1;
+  float g = 0.f;
+  if (lane < p.k) {
+    id = p.ids[t * p.k + lane];
+    g = p.dweights[t * p.k + lane];
+  }
+  L* out = static_cast<L*>(p.dlogits) + t * p.E;
+  if (wide) {
+    constexpr int VEC = 16 / sizeof(L);
+    for (int j = lane * VEC; j < p.E; j += G * VEC)
+      *reinterpret_cast<uint4*>(out + j) = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int j = lane; j < p.E; j += G) store(out + j, 0.f);
+  }
+  if (id >= p.E) {
+    flag(p.status, GG_DEV_BAD_ROUTE);
+    id = -1;
+  }
+  float x = -INFINITY;
+  bool ignored = false;
+  if (id >= 0)
+    x = logit_or_mask(to_float(static_cast<const L*>(p.logits)[t * p.E + id]), &ignored);
+  const bool live = x > -INFINITY;
+  if (!live) id = -1;
+  g = live ? p.scale * g : 0.f;
+  float v, mean = 0.f;
+  if (renorm) {
+    const float m = group_max<G>(mask, sig ? fminf(x, 0.f) : x);
+    v = !live ? 0.f : sig ? sigmoid_over(x, m) : expf(x - m);
+    const float total = group_sum<G>(mask, v);
+    v = live ? v / total : 0.f;  // a true quotient: the share of an only slot is 1, its gradient 0
+    mean = group_sum<G>(mask, g * v);
+    // The mean of what is left takes the first mean's rounding off: gains that hardly differ
+    // keep their differences, whatever the shares.
+    g -= mean;
+    mean = group_sum<G>(mask, live ? g * v : 0.f);
+    if (mean != mean) mean = 0.f;  // an infinite gain: the plain formula's values
+  } else {
+    v = sigmoid(x);
+  }
+  if (sig) v *= sigmoid(-x);  // 1 - sigma(x) = sigma(-x)
+  float dx = v * (g - mean);
+  bool again = false;  // an earlier slot has the same expert
+  for (int q = 0; q + 1 < p.k; ++q) {
+    const int32_t other = __shfl_sync(mask, id, q, G);
+    again |= q < lane && other == id;
+  }
+  again = again && live;
+  if (__any_sync(mask, again)) {  // the first of them takes the others' in their order
+    float sum = dx;
+    for (int q = 1; q < p.k; ++q) {
+      const int32_t other = __shfl_sync(mask, id, q, G);
+      const float more = __shfl_sync(mask, dx, q, G);
+      if (q > lane && other == id) sum += more;
+    }
+    dx = sum;
+  }
+  __syncwarp(mask);  // the zeros come before
+  if (live && !again) store(out + id, dx);
 }
 
 template <int N> using Int = std::integral_constant<int, N>;
@@ -741,7 +761,7 @@ void by_experts(int E, bool few, const F& f) {
 
 // 1 x 64 bf16: 2.2 us a call in a graph with a warp a token, 3.3 us with four lanes; 32768 x
 // 64: 16.2 and 7.3 us. The two break even where the warps fill the GPU (148 SMs x 32 or so).
-// Backward 512 x 64: 2.0 and 3.7 us, 4096 x 64 2.9 and 3.9.
+// Backward from all experts 512 x 64: 2.0 and 3.7 us, 4096 x 64 2.9 and 3.9.
 constexpr int64_t FEW = 4096;
 
 template <typename L, bool BIAS>
@@ -751,7 +771,7 @@ gg_status launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t s
   const bool wide_bias = p.E % 8 == 0 && !misaligned(p.bias, 16);
   // sixteen experts a lane and so more tokens a warp for bf16 (7.3 us for 32768 x 64, 8.3 with
   // eight), eight for fp32, whose looking-up further and checking is shared by few tokens anyway
-  // (16411 x 256 with a bias: 16.5 us, 19.1 with sixteen)
+  // (16411 x 256 with a bias: 14.2 us, a sixth more with sixteen)
   constexpr int MANY = !BIAS && sizeof(L) == 2 ? 16 : 8;
   by_experts<MANY, 2>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
@@ -764,11 +784,23 @@ gg_status launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t s
 template <typename L>
 gg_status launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream_t stream) {
   gg_status s = GG_OK;
+  if (sigmoid || renorm) {
+    const bool wide = p.E * sizeof(L) % 16 == 0 && !misaligned(p.dlogits, 16);
+    const auto go = [&](auto g) {
+      constexpr int G = decltype(g)::value, PER = THREADS / G;
+      return launch("gg_gate_topk_backward", gate_backward_chosen_kernel<L, G>,
+                    (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, sigmoid, renorm, wide);
+    };
+    // a warp writes few tokens' long rows sooner (512 x 1000 bf16: 2.7 us, 3.1 with eight lanes;
+    // 4096 x 1000 4.3 and 4.2, 512 x 64 2.5 and 2.3)
+    if (p.k > 16 || (p.T <= 1024 && p.E * sizeof(L) > 1024)) return go(Int<32>());
+    return p.k <= 8 ? go(Int<8>()) : go(Int<16>());
+  }
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16) && !misaligned(p.dlogits, 16);
   by_experts<16, 4>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
     s = launch("gg_gate_topk_backward", gate_backward_kernel<L, G, NV>,
-               (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, sigmoid, renorm, wide);
+               (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, wide);
   });
   return s;
 }
