@@ -738,30 +738,29 @@ __global__ void __launch_bounds__(THREADS) gate_backward_chosen_kernel(Params p,
 
 template <int N> using Int = std::integral_constant<int, N>;
 
-// Lanes a token and experts a lane (NV, or half as much again where that wastes less). A warp for
-// each token is the quickest for few of them, several tokens a warp the cheapest in instructions
-// for many. (32768 tokens of 160 and of 384 experts, top 6 and 8, bf16: 18.4 and 34.6 us without
-// the halves in between.)
-template <int NV, int LEAST, typename F>
+// Lanes a token and experts a lane: NV, or MORE (half as much again, or three times that) where
+// it wastes less. A warp for each token is the quickest for few of them, several tokens a warp the
+// cheapest in instructions for many. (32768 tokens of 160 and of 384 experts, top 6 and 8, bf16:
+// 12.3 and 21.9 us, 18.4 and 34.6 without MORE.)
+template <int NV, int MORE, int LEAST, typename F>
 void by_experts(int E, bool few, const F& f) {
-  constexpr int MORE_NV = NV + NV / 2;
   if (few && E <= 32 * LEAST) f(Int<32>(), Int<LEAST>());
   else if (few && E <= 128) f(Int<32>(), Int<4>());
   else if (few && E <= 256) f(Int<32>(), Int<8>());
   else if (E <= 64) f(Int<64 / NV>(), Int<NV>());
-  else if (E <= 96) f(Int<64 / NV>(), Int<MORE_NV>());
+  else if (E <= 96) f(Int<96 / MORE>(), Int<MORE>());
   else if (E <= 128) f(Int<128 / NV>(), Int<NV>());
-  else if (E <= 192) f(Int<128 / NV>(), Int<MORE_NV>());
+  else if (E <= 192) f(Int<192 / MORE>(), Int<MORE>());
   else if (E <= 256) f(Int<256 / NV>(), Int<NV>());
-  else if (E <= 384) f(Int<256 / NV>(), Int<MORE_NV>());
+  else if (E <= 384) f(Int<384 / MORE>(), Int<MORE>());
   else if (E <= 512) f(Int<32>(), Int<16>());
   else if (E <= 768) f(Int<32>(), Int<24>());
   else f(Int<32>(), Int<32>());
 }
 
-// 1 x 64 bf16: 2.2 us a call in a graph with a warp a token, 3.3 us with four lanes; 32768 x
-// 64: 16.2 and 7.3 us. The two break even where the warps fill the GPU (148 SMs x 32 or so).
-// Backward from all experts 512 x 64: 2.0 and 3.7 us, 4096 x 64 2.9 and 3.9.
+// 1 x 64 bf16: 1.8 us a call in a graph with a warp a token, 2.6 us with four lanes; 4096 x 64:
+// 2.7 and 3.5, 8192 x 64: 4.1 and 3.8, 32768 x 64: 12.6 and 6.7. Backward from all experts
+// 512 x 64: 1.7 and 3.5, 4096 x 64 2.4 and 3.6 (2.9 at 8192 with eight lanes).
 constexpr int64_t FEW = 4096;
 
 template <typename L, bool BIAS>
@@ -769,15 +768,17 @@ gg_status launch_gate(const Params& p, bool sigmoid, bool renorm, cudaStream_t s
   gg_status s = GG_OK;
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16);
   const bool wide_bias = p.E % 8 == 0 && !misaligned(p.bias, 16);
-  // sixteen experts a lane and so more tokens a warp for bf16 (7.3 us for 32768 x 64, 8.3 with
-  // eight), eight for fp32, whose looking-up further and checking is shared by few tokens anyway
-  // (16411 x 256 with a bias: 14.2 us, a sixth more with sixteen)
-  constexpr int MANY = !BIAS && sizeof(L) == 2 ? 16 : 8;
-  by_experts<MANY, 2>(p.E, p.T <= FEW, [&](auto g, auto nv) {
+  const auto go = [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
     s = launch("gg_gate_topk", gate_kernel<L, G, NV, BIAS>, (unsigned)((p.T + PER - 1) / PER),
                THREADS, stream, p, sigmoid, renorm, wide, wide_bias);
-  });
+  };
+  // eight experts a lane where that fills the GPU better, sixteen and so more tokens a warp for
+  // many (bf16 16411 x 64: 4.4 and 4.8 us, 32768 x 64: 7.5 and 6.7; fp32 with a bias 8192 x 256:
+  // 8.5 and 9.0, 16411 x 256 14.3 both, 32768 x 256: 25.7 and 23.8)
+  constexpr int64_t MANY = sizeof(L) == 2 ? 1 << 21 : 1 << 22;
+  if (p.T * p.E < MANY) by_experts<8, 12, 2>(p.E, p.T <= FEW, go);
+  else by_experts<16, 24, 2>(p.E, p.T <= FEW, go);
   return s;
 }
 
@@ -791,13 +792,15 @@ gg_status launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream
       return launch("gg_gate_topk_backward", gate_backward_chosen_kernel<L, G>,
                     (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, sigmoid, renorm, wide);
     };
-    // a warp writes few tokens' long rows sooner (512 x 1000 bf16: 2.7 us, 3.1 with eight lanes;
+    // a warp writes few tokens' long rows sooner (512 x 1000 bf16: 2.3 us, 3.1 with eight lanes;
     // 4096 x 1000 4.3 and 4.2, 512 x 64 2.5 and 2.3)
     if (p.k > 16 || (p.T <= 1024 && p.E * sizeof(L) > 1024)) return go(Int<32>());
     return p.k <= 8 ? go(Int<8>()) : go(Int<16>());
   }
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16) && !misaligned(p.dlogits, 16);
-  by_experts<16, 4>(p.E, p.T <= FEW, [&](auto g, auto nv) {
+  // eight experts a lane: 32768 x 64 bf16 6.0 us, 16411 x 256 fp32 6.9, with sixteen 6.5 and 8.8;
+  // twelve are no whole vectors of bf16 (32768 x 160: 15.3 us, 9.6 with 24)
+  by_experts<8, 24, 4>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
     s = launch("gg_gate_topk_backward", gate_backward_kernel<L, G, NV>,
                (unsigned)((p.T + PER - 1) / PER), THREADS, stream, p, wide);
