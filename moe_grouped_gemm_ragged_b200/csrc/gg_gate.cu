@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
   if (bad_count && t == 0 && lane == 0) flag(p.status, GG_DEV_BAD_COUNT);
 }
 
-// Gradient of the logits. With v the weights before `scale` and g = scale * dweights:
+// Gradient of the logits. With v the weights before `scale` and g = scale * dweights (scaled last, where only the chosen count):
 //   softmax over all      dx_j = p_j (g_j - sum_i g_i p_i)   (g_j = 0 for the others)
 //   softmax renormalised  dx_i = v_i (g_i - sum g v)
 //   sigmoid               dx_i = g_i s_i (1 - s_i)
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_chosen_kernel(Params p,
     x = logit_or_mask(to_float(static_cast<const L*>(p.logits)[t * p.E + id]), &ignored);
   const bool live = x > -INFINITY;
   if (!live) id = -1;
-  g = live ? p.scale * g : 0.f;
+  g = live ? g : 0.f;
   float v, mean = 0.f;
   if (renorm) {
     const float m = group_max<G>(mask, sig ? fminf(x, 0.f) : x);
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_chosen_kernel(Params p,
     v = sigmoid(x);
   }
   if (sig) v *= sigmoid(-x);  // 1 - sigma(x) = sigma(-x)
-  float dx = v * (g - mean);
+  float dx = p.scale * (v * (g - mean));  // scaled last: differences of dweights are exact
   bool again = false;  // an earlier slot has the same expert
   for (int q = 0; q + 1 < p.k; ++q) {
     const int32_t other = __shfl_sync(mask, id, q, G);
