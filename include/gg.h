@@ -274,8 +274,8 @@ GG_API gg_status gg_route_noalloc(const int32_t* topk_ids, int64_t T_tok, int32_
  *   score      GG_GATE_SOFTMAX: p = softmax(x) over the token's experts;
  *              GG_GATE_SIGMOID: p = 1 / (1 + e^-x)
  *   flags      GG_GATE_RENORM: the weights are scale * p / (sum of the k chosen p), else
- *              scale * p; the sum is taken relative to the largest of the chosen, so it
- *              neither underflows nor overflows
+ *              scale * p; the sum neither underflows nor overflows (it is taken relative to
+ *              the largest of the chosen where it would)
  *   num_tokens int32, device, or NULL (T): tokens in use of a padded batch; the logits of the
  *              others are not read, their ids are -1 and their weights 0
  *   topk_ids   int32 [T, k], best first, ties to the lowest expert (-0 equals +0); weights
