@@ -741,6 +741,24 @@ def test_gate_gradient_of_an_only_expert_is_zero(score, dtype):
         assert bool((dx == 0).all())
 
 
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("shift", [0.0, -10.0, -14.0, -16.0, -60.0, -86.0, -300.0])
+def test_gate_shares_of_scores_far_below_one(shift, biased):
+    """Sigmoid shares keep their precision however small the scores are. In units of U: e^-x 4, the
+    sum under it 1, the quotient 4, their sum as much and its 4 additions, the share's quotient and
+    the scale 2; the difference to the largest, at most 16, moves a share by 16."""
+    gen = torch.Generator().manual_seed(9)
+    x = torch.randn(300, 48, generator=gen) + shift
+    bias = torch.randn(48, generator=gen) if biased else None
+    ids, w = gg.gate_topk(x.cuda(), 5, score=gg.GATE_SIGMOID, scale=2.5,
+                          bias=None if bias is None else bias.cuda())
+    s = np.take_along_axis(x.double().numpy(), ids.cpu().numpy().astype(np.int64), 1)
+    s = -np.logaddexp(0.0, -s)  # their logarithms
+    s = np.exp(s - s.max(1, keepdims=True))
+    ref = 2.5 * s / s.sum(1, keepdims=True)
+    _near(w.cpu().double().numpy(), ref, 48 * U * ref + F32_TINY, "weights")
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_gate_gradient_of_gains_that_hardly_differ(sigmoid):
     """Renormalised weights whose gradients differ in their last bits: dx_i = v_i (g_i - sum g v),
