@@ -232,9 +232,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
           const float2 su = __fmul2_rn(silu, u[j]), sd = __fmul2_rn(d[j], both(scale));
           dots = __ffma2_rn(d[j], su, dots);
           a[j] = __fmul2_rn(su, both(scale));
-          // q + silu - silu q
-          const float2 slope =
-              __ffma2_rn(make_float2(-silu.x, -silu.y), q, __fadd2_rn(q, silu));
+          // q + silu (1 - q): 1 - q first, as silu beside it can be past 2^24, where q has no
+          // part in their sum
+          const float2 slope = __ffma2_rn(silu, __ffma2_rn(both(-1.f), q, both(1.f)), q);
           g[j] = __fmul2_rn(__fmul2_rn(sd, u[j]), slope);
           u[j] = __fmul2_rn(sd, silu);
         }
