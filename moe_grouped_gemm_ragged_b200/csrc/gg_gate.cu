@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(THREADS) gate_kernel(Params p, bool sigmoid, b
   if (bad_count && t == 0 && lane == 0) flag(p.status, GG_DEV_BAD_COUNT);
 }
 
-// Gradient of the logits. With v the weights before `scale` and g = scale * dweights (scaled last, where only the chosen count):
+// Gradient of the logits. With v the weights before `scale` and g = scale * dweights (scaled
+// last: differences of dweights are exact):
 //   softmax over all      dx_j = p_j (g_j - sum_i g_i p_i)   (g_j = 0 for the others)
 //   softmax renormalised  dx_i = v_i (g_i - sum g v)
 //   sigmoid               dx_i = g_i s_i (1 - s_i)
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool w
 #pragma unroll 1
   for (int s = lane; s < p.k; s += G) {
     int32_t id = p.ids[t * p.k + s];
-    float g = p.scale * p.dweights[t * p.k + s];
+    float g = p.dweights[t * p.k + s];
     bad |= id >= p.E;
     if (id < 0 || id >= p.E) id = -1, g = 0.f;
     c.id[s] = id;
@@ -656,10 +657,27 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool w
     total += x[j];
     mean = fmaf(x[j], out[j], mean);
   }
-  const float inv = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 1e-30f));
+  // the total is 1 or more unless all of them are masked
+  const float inv = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 0.5f));
   mean = group_sum<G>(mask, mean) * inv;
+  // Gains of the probable experts that hardly differ (one expert with nearly all of it) cancel
+  // against the mean: the mean of what is left takes its rounding off.
+  float2 pairs = both(0.f);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) out[j] = x[j] * inv * (out[j] - mean);
+  for (int j = 0; j < NV; j += 2) {
+    const float2 d = __fadd2_rn(make_float2(out[j], out[j + 1]), both(-mean));
+    pairs = __ffma2_rn(make_float2(x[j], x[j + 1]), d, pairs);
+    out[j] = d.x, out[j + 1] = d.y;
+  }
+  float rest = group_sum<G>(mask, pairs.x + pairs.y) * inv;
+  if (rest != rest) rest = 0.f;  // an infinite gain: the plain formula's values
+  const float2 share = both(p.scale * inv);
+#pragma unroll
+  for (int j = 0; j < NV; j += 2) {
+    const float2 d = __fadd2_rn(make_float2(out[j], out[j + 1]), both(-rest));
+    const float2 dx = __fmul2_rn(__fmul2_rn(make_float2(x[j], x[j + 1]), share), d);
+    out[j] = dx.x, out[j + 1] = dx.y;
+  }
   store_row<NV>(static_cast<L*>(p.dlogits) + t * p.E, lane * NV, p.E, wide, out);
   if (bad) flag(p.status, GG_DEV_BAD_ROUTE);
 }

@@ -76,3 +76,50 @@ def test_silu_mul_of_large_gates(rows, N, concat, ckpt):
     g = sizes * rng.uniform(1, 2, (rows, N // 2)) * rng.choice([-1, 1], (rows, N // 2))
     u, d = (2.0 ** -20 * rng.normal(size=(rows, N // 2)) for _ in range(2))
     _check_silu_mul(g, u, d, rng.normal(size=rows), concat, ckpt, 8)
+
+
+# ------------------------------------------------------------------------------------- gate
+
+@pytest.mark.parametrize("T,E,k", [(40, 7, 2), (64, 64, 4), (30, 160, 6), (12, 1000, 8),
+                                   (4200, 64, 1), (4200, 64, 8), (4200, 200, 5)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gate_gradient_of_a_confident_expert(T, E, k, dtype):
+    """Softmax over all experts with one of them 8 to 20 above the rest: its gradient
+    p (g - sum p_i g_i) = p sum p_i (g - g_i) is many times smaller than g. In units of U: a power
+    is off by 4 and 1.3 times its argument (25 at most), the total and the mean by one of these each, by E / 8
+    additions in a lane and 5 + 5 over the lanes, and there are a few products."""
+    gen = torch.Generator().manual_seed(E + k)
+    x = torch.randn(T, E, generator=gen).clamp(-2.5, 2.5)
+    top = torch.randint(0, E, (T, 1), generator=gen)
+    x.scatter_(1, top, 2.5 + 8 + 12 * torch.rand(T, 1, generator=gen))
+    x = (x + torch.randn(T, 1, generator=gen)).to(dtype)
+    for gains in (torch.ones(T, k), torch.randn(T, k, generator=gen)):
+        ids, _ = gg.gate_topk(x.cuda(), k, renorm=False, scale=2.5)
+        dx = gg.gate_topk_backward(x.cuda(), ids, gains.cuda(), renorm=False, scale=2.5)
+        ids = ids.cpu().numpy()
+        assert (ids[:, :1] == top.numpy()).all()
+        x64, g64 = x.double().numpy(), gains.double().numpy()
+        ref = ol.gate_backward(x64, ids, g64, renorm=False, scale=2.5)
+        p, g = ol._softmax(x64), np.zeros((T, E))
+        np.put_along_axis(g, ids.astype(np.int64), g64, 1)
+        far = np.abs(g - g64[:, :1])  # gains as they differ from the confident expert's
+        size = 2.5 * p * (far + (p * far).sum(1, keepdims=True))
+        units = 3 * (4 + 1.3 * 25) + E / 8 + 26
+        bound = size * units * U + F32_TINY
+        if dtype is torch.bfloat16:
+            bound = bound + np.abs(ref) * B
+        _near(dx.cpu().double().numpy(), ref, bound, "dlogits")
+
+
+def test_gate_gradient_of_infinite_and_missing_gains():
+    """An infinite gain of the best expert takes every other gradient to minus infinity, as the
+    formula has it; a token without ids has zeros whatever its gains are."""
+    x = torch.randn(3, 64, generator=torch.Generator().manual_seed(3)).cuda()
+    ids, w = gg.gate_topk(x, 4, renorm=False)
+    ids[1] = -1
+    dw = torch.ones_like(w)
+    dw[0, 0], dw[1] = float("inf"), float("nan")
+    dx = gg.gate_topk_backward(x, ids, dw, renorm=False)
+    others = torch.arange(64, device="cuda") != ids[0, 0]
+    assert bool((dx[0][others] == -float("inf")).all()) and bool(dx[0][~others].isnan())
+    assert bool((dx[1] == 0).all()) and bool(torch.isfinite(dx[2]).all())
