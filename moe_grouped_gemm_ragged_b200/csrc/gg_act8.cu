@@ -44,9 +44,10 @@ struct Params {
   int32_t zero_tail;
 };
 
-// sigma(x) = 1 / (1 + 2^(-x log2 e)) of a pair, by the hardware's powers and reciprocals: off by
-// 1 + |x| log2 e units of 2^-23 or so, against half a step of 2^-8 in the bf16 results. Numbers
-// below 2^-126 count as 0.
+// sigma(x) = 1 / (1 + 2^(-x log2 e)) of a pair, by the hardware's powers and reciprocals. In units
+// of 2^-23 the power is off by 2 + 0.62 |x| (its own error; its argument's two roundings), the sum by
+// 0.5, the reciprocal by 1: 3.5 + 0.62 |x| at most, against half a step of 2^-8 in the bf16 results.
+// Below 2^-126 (x < -87.3) it is 0: such gates are done over (FAR).
 __device__ __forceinline__ float2 sigmoid(const float2& x) {
   float2 t = __fmul2_rn(x, both(-1.44269504f));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));
@@ -55,6 +56,52 @@ __device__ __forceinline__ float2 sigmoid(const float2& x) {
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.x));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.y));
   return t;
+}
+
+// One pair of each direction. h = [g, u] from its 8 bits (or bf16), s the row's weight, q =
+// sigma(g):
+//   dg = s dact u (q + g q (1 - q)),  du = s dact g q,  act = s g q u,  ds = <dact, g q u>
+__device__ __forceinline__ float2 silu_times(const float2& g, const float2& u) {
+  return __fmul2_rn(__fmul2_rn(g, sigmoid(g)), u);
+}
+struct Gradient {
+  float2 su, dg, du;  // g q u without the weight, and the two gradients
+};
+__device__ __forceinline__ Gradient gradient(const float2& g, const float2& u, const float2& sd) {
+  const float2 q = sigmoid(g), silu = __fmul2_rn(g, q);
+  // 1 - q first, as silu can be past 2^24, where q has no part in their sum
+  const float2 slope = __ffma2_rn(silu, __ffma2_rn(both(-1.f), q, both(1.f)), q);
+  return {__fmul2_rn(silu, u), __fmul2_rn(__fmul2_rn(sd, u), slope), __fmul2_rn(sd, silu)};
+}
+
+// Gates under -87: fp32 holds their sigma (then e^g to the last bit) badly or not at all, while
+// bf16 holds g sigma(g) u down to 2^-133. Their products are made with the fourth root of e^g, one
+// factor after the other. A vector that may have one is told by its bits, or by its block's code.
+constexpr float FAR = -87.f;
+constexpr uint32_t FAR_BITS = 0xc2af0000u;  // -87.5, the next bf16, in the upper half of a word
+constexpr uint32_t FAR_CODE = 125;          // the least with which a block can hold 87: 448 / 4
+
+__device__ __forceinline__ bool any_far(const uint4& v) {  // of eight bf16: -87.5 or further down
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x, v.y), __vmaxu2(v.z, v.w));
+  return m >= FAR_BITS || (m << 16) >= FAR_BITS;
+}
+__device__ __forceinline__ float fourth_root(float g) {  // of e^g
+  float t = g * 0.36067376f;
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t));
+  return t;
+}
+__device__ __forceinline__ void silu_times_far(float g, float u, float& su) {
+  if (!(g < FAR)) return;
+  const float e = fourth_root(g);
+  su = g * e * u * e * e * e;
+}
+__device__ __forceinline__ void gradient_far(float g, float u, float sd, float& su, float& dg,
+                                             float& du) {
+  if (!(g < FAR)) return;
+  const float e = fourth_root(g);
+  su = g * e * u * e * e * e;
+  dg = sd * u * e * (1.f + g) * e * e * e;
+  du = g * e * sd * e * e * e;
 }
 
 // A row belongs to G lanes of a warp (W 1), or to all W warps of a block (G 32). They take its
@@ -111,6 +158,30 @@ __device__ __forceinline__ int64_t up_code(const Params& p, int c) {
   return p.concat ? (c >> 2) + (p.half + kBlock - 1) / kBlock : gate_code(p, c) + 4;
 }
 
+// A thread's vectors with far gates, done over when the rest is done. (Beside the rest, as in the
+// backward pass, it takes registers that the 8 bits need: 65536 x 4096 231 us, 169 like this. The
+// backward pass may have written dH or act over its inputs by then; beside the rest it takes 46.8
+// and 50.0 us for 32768 x 1536 from 8 bits and from bf16, 45.6 and 48.6 without it.)
+__device__ __noinline__ void silu_mul_far(const uint4* H, uint4* act, int32_t concat, int vecs,
+                                          int c, int step, float scale) {
+  for (; c < vecs; c += step) {
+    const int64_t at = concat ? c : (c >> 4) * 32 + (c & 15);
+    const uint4 gv = H[at];
+    if (!any_far(gv)) continue;
+    float2 g[4], u[4];
+    unpack_bf16(gv, g);
+    unpack_bf16(H[at + (concat ? vecs : 16)], u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float2 a = silu_times(g[j], u[j]);
+      silu_times_far(g[j].x, u[j].x, a.x);
+      silu_times_far(g[j].y, u[j].y, a.y);
+      g[j] = __fmul2_rn(a, both(scale));
+    }
+    act[c] = pack_bf16(g);
+  }
+}
+
 template <int G, int W, int U, bool CKPT>
 __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
   after_previous();
@@ -128,6 +199,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
   if (row < 0) return;
   const int64_t base = row * 2 * vecs;
   const int64_t code0 = row * 2 * ((p.half + kBlock - 1) / kBlock);
+  bool far = false;
   // a row's lanes go round together: the four lanes of a block exchange their largest values
   for (int c0 = first_vec<G, W, U>(); c0 - (int)(threadIdx.x % G) < vecs; c0 += W * U * G) {
     uint4 gv[U], uv[U];
@@ -152,6 +224,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
         uint32_t cg, cu;
         bool odd;
         block_codes(row_mask<G>(), gv[i], uv[i], cg, cu, &odd);
+        far |= cg >= FAR_CODE;
         if (c < vecs) {
           p.H8_out[base + gate_vec(p, c)] = to_e4m3(g, cg, odd);
           p.H8_out[base + up_vec(p, c)] = to_e4m3(u, cu, odd);
@@ -162,17 +235,18 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
         }
       }
       if (c < vecs) {
+        if constexpr (!CKPT) far |= any_far(gv[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          g[j] = __fmul2_rn(__fmul2_rn(__fmul2_rn(g[j], sigmoid(g[j])), u[j]), both(scale));
+        for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(silu_times(g[j], u[j]), both(scale));
         p.act[row * vecs + c] = pack_bf16(g);
       }
     }
   }
+  if (far)
+    silu_mul_far(p.H + base, p.act + row * vecs, p.concat, vecs, first_vec<G, W, U>(), W * G,
+                 scale);
 }
 
-// h = [g, u] from its 8 bits (or bf16), s the row's weight, q = sigma(g):
-//   dg = s dact u (q + g q (1 - q)),  du = s dact g q,  act = s g q u,  ds = <dact, g q u>
 template <int G, int W, int U, bool FROM8>
 __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Params p) {
   after_previous();
@@ -218,25 +292,29 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_backward_kernel(Para
         const int c = c0 + G * i;
         if (c >= vecs) continue;
         float2 g[4], u[4], d[4], a[4];
+        bool far;
         if constexpr (FROM8) {
           from_e4m3(g8[i], code_scale(cg[i]), g);
           from_e4m3(u8[i], code_scale(cu[i]), u);
+          far = cg[i] >= FAR_CODE;
         } else {
           unpack_bf16(gv[i], g);
           unpack_bf16(uv[i], u);
+          far = any_far(gv[i]);
         }
         unpack_bf16(dv[i], d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 q = sigmoid(g[j]), silu = __fmul2_rn(g[j], q);
-          const float2 su = __fmul2_rn(silu, u[j]), sd = __fmul2_rn(d[j], both(scale));
-          dots = __ffma2_rn(d[j], su, dots);
-          a[j] = __fmul2_rn(su, both(scale));
-          // q + silu (1 - q): 1 - q first, as silu beside it can be past 2^24, where q has no
-          // part in their sum
-          const float2 slope = __ffma2_rn(silu, __ffma2_rn(both(-1.f), q, both(1.f)), q);
-          g[j] = __fmul2_rn(__fmul2_rn(sd, u[j]), slope);
-          u[j] = __fmul2_rn(sd, silu);
+          const float2 sd = __fmul2_rn(d[j], both(scale));
+          Gradient r = gradient(g[j], u[j], sd);
+          if (far) {
+            gradient_far(g[j].x, u[j].x, sd.x, r.su.x, r.dg.x, r.du.x);
+            gradient_far(g[j].y, u[j].y, sd.y, r.su.y, r.dg.y, r.du.y);
+          }
+          dots = __ffma2_rn(d[j], r.su, dots);
+          a[j] = __fmul2_rn(r.su, both(scale));
+          g[j] = r.dg;
+          u[j] = r.du;
         }
         p.dH[base + gate_vec(p, c)] = pack_bf16(g);
         p.dH[base + up_vec(p, c)] = pack_bf16(u);

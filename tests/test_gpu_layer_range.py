@@ -78,6 +78,20 @@ def test_silu_mul_of_large_gates(rows, N, concat, ckpt):
     _check_silu_mul(g, u, d, rng.normal(size=rows), concat, ckpt, 8)
 
 
+@pytest.mark.parametrize("rows,N,concat", [(33, 256, False), (33, 80, True), (1300, 1040, True)])
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_silu_mul_of_far_negative_gates(rows, N, concat, ckpt):
+    """Gates whose sigma is below fp32's normal numbers (-87.3) and then below fp32 itself: bf16
+    holds g sigma(g) u down to 2^-133. sigma's power is off by 4 U for each of the factors that it
+    is made of (four at most) and 1.3 times its argument, and there are a dozen products."""
+    rng = np.random.default_rng(N)
+    g = -np.array([60, 80, 87, 88, 89, 92, 100, 120, 150, 172, 180])[np.arange(rows) % 11, None]
+    g = g * rng.uniform(1, 1.06, (rows, N // 2))
+    u = np.exp2(rng.uniform(80, 126, (rows, N // 2))) * rng.choice([-1, 1], (rows, N // 2))
+    d = 2.0 ** -3 * rng.normal(size=(rows, N // 2))
+    _check_silu_mul(g, u, d, rng.normal(size=rows) / 16, concat, ckpt, 16 + 1.3 * 192 + 16)
+
+
 # ------------------------------------------------------------------------------------- gate
 
 @pytest.mark.parametrize("T,E,k", [(40, 7, 2), (64, 64, 4), (30, 160, 6), (12, 1000, 8),
