@@ -16,6 +16,7 @@ import os
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # GG_LIBRARY may name another build of the same library (e.g. with other tuning macros)
@@ -477,6 +478,15 @@ def route(topk_ids: torch.Tensor, X: torch.Tensor, E: int, *,
     return A_packed, row_of, offs
 
 
+def _wants_grad(*tensors) -> bool:
+    """Whether a call's result depends on a tensor that gradients are kept of. A tensor with a
+    tangent is refused: it would be lost without a word."""
+    if getattr(forward_ad, "_current_level", 0) >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("forward-mode differentiation is not supported")
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 class _GroupedMM(torch.autograd.Function):
     """out = grouped A @ W over the offsets; backward runs dgrad and wgrad on the same
     groups. Output and input gradient are complete tensors (zero past the last offset)."""
@@ -520,7 +530,7 @@ def grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torch.Tensor,
     offset are zero in the output and in dA. Without autograd, ``out`` may be given (rows
     past the last offset are then left as they are). With ``ckpt8`` A is kept for the wgrad in
     8 bits (``pack8``), about half its bytes, and dW is the product with these values."""
-    if torch.is_grad_enabled() and (A.requires_grad or W.requires_grad):
+    if _wants_grad(A, W):
         if out is not None:
             raise ValueError("out= cannot be used with autograd")
         return _GroupedMM.apply(A, W, offs, w_nk, ckpt8)

@@ -5,8 +5,8 @@ back, ``silu_mul`` stands between the two expert products, ``pack8`` keeps rows 
 with its gradient, as thin calls of the C ABI that write into the caller's buffers (buffers left
 as None are allocated, uninitialised, for the stream that the call runs on). ``gate``,
 ``dispatch``, ``swiglu``, ``expert_mlp`` and ``combine`` are the same operators with autograd, to
-stand beside ``grouped_mm``; they run on the current stream, and their backward passes do not
-support being differentiated again.
+stand beside ``grouped_mm``; they run on the current stream, their backward passes do not support
+being differentiated again, and tensors with a tangent (forward-mode differentiation) are refused.
 
 Capture in a CUDA graph: the calls that write into buffers need nothing but their buffers. A
 backward pass of the autograd forms can be captured like any other of torch: together with its
@@ -22,7 +22,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (FLAG_GATE_UP_CONCAT, FLAG_ZERO_TAIL, _check, _raise, _status_ptr, _stream_handle,
-               dgrad_ex, forward_ex, lib, route, wgrad_ex)
+               _wants_grad, dgrad_ex, forward_ex, lib, route, wgrad_ex)
 
 try:  # csrc/binding.cpp: the calls below with their buffers in hand, 3 us sooner
     from . import _native
@@ -418,10 +418,6 @@ def _dense(g: torch.Tensor) -> torch.Tensor:
     """A gradient as the kernels take it: contiguous, on a 16-byte boundary."""
     g = g.contiguous()
     return g if g.data_ptr() % 16 == 0 else g.clone()
-
-
-def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 class _Gate(torch.autograd.Function):
