@@ -17,6 +17,7 @@ from typing import Optional
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # GG_LIBRARY may name another build of the same library (e.g. with other tuning macros)
@@ -506,6 +507,7 @@ class _GroupedMM(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         A, W, offs, A8, scale = ctx.saved_tensors
         dout = dout.contiguous()

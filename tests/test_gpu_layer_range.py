@@ -137,3 +137,18 @@ def test_gate_gradient_of_infinite_and_missing_gains():
     others = torch.arange(64, device="cuda") != ids[0, 0]
     assert bool((dx[0][others] == -float("inf")).all()) and bool(dx[0][~others].isnan())
     assert bool((dx[1] == 0).all()) and bool(torch.isfinite(dx[2]).all())
+
+
+# ------------------------------------------------------------------------------- autograd
+
+@pytest.mark.parametrize("ckpt8", [False, True])
+def test_grouped_mm_refuses_a_second_derivative(ckpt8):
+    """The gradients are not functions that can be differentiated again: asking for it is an
+    error, not a gradient without those terms."""
+    A = torch.randn(32, 64, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    W = torch.randn(2, 64, 64, device="cuda").to(torch.bfloat16).requires_grad_(True)
+    offs = torch.tensor([16, 32], dtype=torch.int32, device="cuda")
+    out = gg.grouped_mm(A, W, offs, ckpt8=ckpt8)
+    dA, dW = torch.autograd.grad(out.float().pow(2).sum(), (A, W), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (dA.float().sum() + dW.float().sum() + A.float().sum()).backward()
