@@ -1,8 +1,10 @@
 """Build step of the CUDA library: nvcc for sm_100a into ``libgg.so`` next to this file, and of
-the Python module ``_native`` (``csrc/binding.cpp``, the quick way into the layer's calls).
+the Python module ``_native_...`` (``csrc/binding.cpp``, the quick way into the layer's calls).
 
 Run ``python -m moe_grouped_gemm_ragged_b200._build`` (or call :func:`build`). Each is rebuilt
-when a source of its own under ``csrc/`` or ``include/`` is newer than it.
+when a source of its own under ``csrc/`` or ``include/`` is newer than it. The module reads torch's
+tensors through what it was compiled against, so its name tells that torch: another torch finds
+none, makes its own, or goes without.
 """
 from __future__ import annotations
 
@@ -11,6 +13,12 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
+
+try:
+    from ._native_name import native_name
+except ImportError:  # run as a file
+    from _native_name import native_name
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,8 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgg.so")
 BINDING = os.path.join(CSRC, "binding.cpp")
-# for this interpreter only: another one does not find it and goes without
-NATIVE = os.path.join(PKG, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))
+# for this interpreter and this torch only: others do not find it
+NATIVE = os.path.join(PKG, native_name() + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -52,15 +60,26 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, out: str = None, defines=()) -> str:
-    """Compile ``csrc/*.cu`` into ``libgg.so`` (sm_100a) unless it is up to date.
+    """Compile ``csrc/*.cu`` into ``libgg.so`` (sm_100a) unless it is up to date, then the Python
+    module; where that cannot be compiled, a warning says so.
 
     ``out`` and ``defines`` (``NAME=VALUE`` strings) build another copy with other tuning
     macros; such a copy is always rebuilt."""
     target = out or LIB
+    if out is not None or force or stale():
+        _build_library(target, verbose, defines)
     if out is None:
-        build_binding(force, verbose)
-        if not force and not stale():
-            return LIB
+        try:
+            build_binding(force, verbose)
+        except (subprocess.CalledProcessError, OSError, ImportError) as e:
+            if os.path.exists(NATIVE):  # of older sources
+                os.remove(NATIVE)
+            warnings.warn(f"csrc/binding.cpp could not be built ({e}); the layer's calls go "
+                          "through ctypes, some microseconds slower", RuntimeWarning)
+    return target
+
+
+def _build_library(target: str, verbose: bool, defines) -> None:
     tmp = target + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-I", CSRC,
            *sources(), "-o", tmp]
@@ -69,7 +88,6 @@ def build(force: bool = False, verbose: bool = False, out: str = None, defines=(
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, target)
-    return target
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
@@ -86,6 +104,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     tmp = NATIVE + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-DGG_MODULE={native_name()}",
            *[f"-I{d}" for d in cpp_extension.include_paths()],
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
            "-I", INCLUDE, BINDING, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch",

@@ -16,6 +16,7 @@ the stream of the graph that used it first, and a capture cannot wait for that s
 from __future__ import annotations
 
 import ctypes
+import importlib
 from typing import Optional
 
 import torch
@@ -23,11 +24,19 @@ from torch.autograd.function import once_differentiable
 
 from . import (FLAG_GATE_UP_CONCAT, FLAG_ZERO_TAIL, _check, _raise, _status_ptr, _stream_handle,
                _wants_grad, dgrad_ex, forward_ex, lib, route, wgrad_ex)
+from ._native_name import native_name
 
-try:  # csrc/binding.cpp: the calls below with their buffers in hand, 3 us sooner
-    from . import _native
-except ImportError:  # not built for this interpreter: the same through ctypes
-    _native = None
+
+def _load_native():
+    """csrc/binding.cpp: the calls below with their buffers in hand, 3 us sooner. None where it is
+    not built for this interpreter and this torch: the same through ctypes."""
+    try:
+        return importlib.import_module("." + native_name(), __package__)
+    except ImportError:
+        return None
+
+
+_native = _load_native()
 
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 GATE_RENORM, GATE_LOGITS_F32 = 0x1, 0x2
@@ -40,6 +49,9 @@ _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of this module's entry points."""
+    global _native
+    if _native is None:  # built since this module was imported
+        _native = _load_native()
     P, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
     for name, args in {
         "gg_gate_topk": [P, i64, i32, i32, P, i32, i32, f32, P, P, P, P, P],

@@ -388,8 +388,13 @@ PyMethodDef g_methods[] = {GG_METHOD(bind),
                            GG_METHOD(pack8),
                            GG_METHOD(unpack8),
                            {nullptr, nullptr, 0, nullptr}};
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods};
+// GG_MODULE: the module's name, which the build makes of the torch it is compiled against
+#define GG_NAME2(prefix, name) prefix##name
+#define GG_NAME(prefix, name) GG_NAME2(prefix, name)
+#define GG_TEXT2(name) #name
+#define GG_TEXT(name) GG_TEXT2(name)
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, GG_TEXT(GG_MODULE), nullptr, -1, g_methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__native() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC GG_NAME(PyInit_, GG_MODULE)() { return PyModule_Create(&g_module); }
