@@ -300,7 +300,7 @@ GG_API gg_status gg_gate_topk(const void* logits, int64_t T, int32_t E, int32_t 
 /* Gradient of the logits of gg_gate_topk from dweights fp32 [T, k]; score, flags and scale as
    in the forward call, topk_ids its result (slots of id -1 carry nothing). dlogits, in the
    logits' type, is written in full: 0 for every logit that the weights do not depend on, and
-   for tokens without an id. Not in place (dlogits must not overlap logits). */
+   for tokens without an id. Not in place: dlogits that overlaps logits is GG_ERR_INVALID_ARG. */
 GG_API gg_status gg_gate_topk_backward(const void* logits, int64_t T, int32_t E, int32_t k,
                                        int32_t score, int32_t flags, float scale,
                                        const int32_t* topk_ids, const float* dweights,

@@ -171,7 +171,8 @@ def gate_topk_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: t
                        renorm: bool = True, scale: float = 1.0,
                        status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the logits (in their type, written in full) from that of the weights;
-    ``topk_ids`` is what ``gate_topk`` returned for the same score, renorm and scale."""
+    ``topk_ids`` is what ``gate_topk`` returned for the same score, renorm and scale. Not in place:
+    ``dlogits`` must not overlap the logits."""
     if _native is not None:
         rc = _native.gate_topk_backward(logits, topk_ids, dweights, dlogits, score, renorm, scale,
                                         status, stream)

@@ -893,6 +893,8 @@ gg_status gg_gate_topk_backward(const void* logits, int64_t T, int32_t E, int32_
   if (T > 0 && (logits == nullptr || topk_ids == nullptr || dweights == nullptr ||
                 dlogits == nullptr))
     return GG_ERR_INVALID_ARG;
+  // zeros are written before the chosen experts' logits are read
+  if (overlap(logits, dlogits, T * E * (f32 ? 4 : 2))) return GG_ERR_INVALID_ARG;
   int sms = 0;
   if ((s = device_sms(&sms)) != GG_OK) return s;
   if (T == 0) return GG_OK;

@@ -22,6 +22,12 @@ inline bool misaligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
 }
 
+// Whether two arrays of n bytes share any.
+inline bool overlap(const void* a, const void* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < (uintptr_t)n;
+}
+
 // Launch with programmatic dependent launch, as the grouped GEMM's kernels: a kernel may be
 // scheduled while the one before it on the stream finishes, and waits for that one's completion
 // (after_previous, first thing in every thread) before it touches memory. A stream or capture
