@@ -32,7 +32,8 @@
  * Memory. All pointers are device pointers owned by the caller, on the device that is
  * current when the call is made (the kernels run there); bf16 arrays are row major
  * (last index contiguous) and 16-byte aligned. W is one packed [E,K,N] buffer (the single
- * grouped weight of TransformerEngine PR 3224). K and N must be multiples of 8.
+ * grouped weight of TransformerEngine PR 3224). K and N must be multiples of 8. An output shares
+ * no memory with another array of its call, except where a description says that it may.
  *
  * Untouched regions (TransformerEngine PR 3542, "Changes": outputs live in buffers the caller
  * owns, and their rows beyond the used capacity keep their contents):
@@ -342,7 +343,8 @@ GG_API gg_status gg_unroute_backward(const void* dout, const void* Y, int64_t ro
  * Rows: r < *rows_used (int32, device, e.g. &offs[E-1]; NULL: all rows), weight = weights[r];
  * or, with row_of int32 [n_assign], r = row_of[i] and weight = weights[i] for assignment i (the
  * routing weights in the order of gg_gate_topk; entries distinct or -1, below *rows_used where
- * that is given; n_assign 0 names no row). weights NULL: 1. Other rows reach no result and are not written, but with
+ * that is given; n_assign 0 names no row). weights fp32 [rows] or, with row_of, [n_assign] (all of
+ * it may be read); NULL: 1. Other rows reach no result and are not written, but with
  * GG_FLAG_ZERO_TAIL the rows of act at and past *rows_used become +0.0.
  *   act bf16 [rows, I]; H8 e4m3 [rows, N] in the columns' order of H and H8_scale uint8
  *   [rows, 2 * ceil(I / 32)] (both or neither NULL): the 8-bit form of gg_pack8, with blocks of

@@ -16,9 +16,9 @@ constexpr int WARPS = THREADS / 32;
 constexpr uint32_t ALL = 0xffffffffu;
 // Pieces of 32 vectors that a warp takes at once. 64 registers a thread (four blocks an SM) hold
 // four of them; the backward pass, with twice the values a piece, two. us for 65536 rows of
-// 4096 columns, forward and backward: 177 and 257 with four, 188 and 217 with two (the bytes at
-// the copy rate: 168 and 209); 262144 x 6144 to 8 bits and back: 807 and 817 with four, 867 and
-// 828 with two (764 each).
+// 4096 columns, forward and backward with the 8 bits: 169 and 266 with four, 177 and 213 with two
+// (the bytes at the copy rate: 168 and 209); without them 119 and 332, 123 and 250 (125 and 250);
+// 262144 x 6144 to 8 bits and back: 729 and 737 with four, 791 and 752 with two (757 each).
 constexpr int BLOCKS = 4;
 constexpr int MANY = 4, MANY_BACKWARD = 2;
 
@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) unpack8_kernel(
 
 // All warps of a block share a row where there are few of them (more than one piece each, or
 // there is nothing to share): a warp a row would leave most of the GPU idle. us a call in a
-// graph, shared and not, forward: 8 x 1536 2.0 and 3.3, 8 x 16384 3.9 and 18.3, 1001 x 4096 4.2
-// and 6.2; 2048 x 1536 5.5 and 4.2.
+// graph, shared and not, forward with the 8 bits: 8 x 1536 1.8 and 2.9, 8 x 16384 3.9 and 18.4,
+// 1001 x 4096 4.0 and 5.8; 2048 x 1536 5.3 and 3.8 (backward 1.8 and 3.4, 4.0 and 20.5, 4.7 and
+// 6.5; 6.0 and 4.1).
 bool share_row(int64_t items, int64_t vecs, int sms) {
   return vecs > 32 && items <= 8 * (int64_t)sms;
 }
@@ -452,8 +453,9 @@ Params params(int64_t rows, int64_t N, const int32_t* row_of, const float* weigh
 }
 
 // Calls f with the lanes a row: as many as hold it in U pieces, four (the lanes of a block of 32
-// columns) to a warp. 262144 rows of 64 columns to 8 bits take 14 us with four lanes, 64 with a
-// warp; SiLU-and-mul of as many rows of 256 columns 55 with eight lanes, 126.
+// columns) to a warp. 262144 rows of 64 columns to 8 bits take 12 us with four lanes, 56 with a
+// warp; SiLU-and-mul of as many rows of 256 columns 55 with four lanes, 112 (backward 69 with
+// eight, 135).
 template <int N> using Int = std::integral_constant<int, N>;
 template <int U, typename F>
 void by_length(int64_t vecs, const F& f) {

@@ -175,8 +175,9 @@ __device__ __forceinline__ float sigmoid(float x) {
 // numbers loses is then under 2^-129 of the sum. Else of scores relative to the largest.
 constexpr float PLAIN = 0x1p-20f;
 
-// e^x for x <= 0 by the hardware's power: off by 2 + |x| / 2 units of 2^-23, which a sum of a
-// token's exponentials, the large ones of which have small |x|, hardly shows. 0 of -inf.
+// e^x for x <= 0 by the hardware's power: off by 2 units of 2^-23 of its own and 0.62 |x| of its
+// argument's roundings (the product's half unit and log2 e's tenth), which a sum of a token's
+// exponentials, the large ones of which have small |x|, hardly shows. 0 of -inf.
 __device__ __forceinline__ float fast_exp(float x) {
   float t = x * 1.44269504f;
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t));
@@ -184,7 +185,7 @@ __device__ __forceinline__ float fast_exp(float x) {
 }
 
 // The score that a biased choice tries first. In units of 2^-23 it is off by at most
-// sigma (1 - sigma) (2 + 1.17 |x|) < 0.6 from the fast exponential, 2.5 from the sum and the
+// sigma (1 - sigma) (2 + 0.62 |x|) < 0.6 from the fast exponential, 2.5 from the sum and the
 // reciprocal and (1 + |bias|) / 2 from the last sum; two scores further apart than CLOSE
 // (1 + |bias| + |bias'|) are in the right order, with half of CLOSE to spare.
 __device__ __forceinline__ float fast_score(float x, float b) {
@@ -199,7 +200,9 @@ constexpr float CLOSE = 16.f / 8388608.f;
 // fp32 orders are looked up past the k-th until it is seen that no other expert may belong to
 // the chosen, one place most often and this many at most. (With a fixed two places about one
 // biased token in ten thousand of 256 experts stayed open, and one such token adds 4 us to a
-// call.)
+// call.) Where more logits than these are equal at the k-th place, a token goes on to all of its
+// experts' doubles: batches of nothing but zeros take 37 us of 32768 x 64 fp32 (10.6 of random
+// logits) and 54 of 16411 x 256 (11.9), 65 under a bias (14.5).
 constexpr int MORE = 4;
 
 template <int SLOTS>
@@ -661,7 +664,8 @@ __global__ void __launch_bounds__(THREADS) gate_backward_kernel(Params p, bool w
   const float inv = __fdividef(1.f, fmaxf(group_sum<G>(mask, total), 0.5f));
   mean = group_sum<G>(mask, mean) * inv;
   // Gains of the probable experts that hardly differ (one expert with nearly all of it) cancel
-  // against the mean: the mean of what is left takes its rounding off.
+  // against the mean: the mean of what is left takes its rounding off (32768 x 64 bf16 6.2 us for
+  // 6.05, 16411 x 256 fp32 7.3 for 6.95).
   float2 pairs = both(0.f);
 #pragma unroll
   for (int j = 0; j < NV; j += 2) {
@@ -778,7 +782,7 @@ void by_experts(int E, bool few, const F& f) {
 
 // 1 x 64 bf16: 1.8 us a call in a graph with a warp a token, 2.6 us with four lanes; 4096 x 64:
 // 2.7 and 3.5, 8192 x 64: 4.1 and 3.8, 32768 x 64: 12.6 and 6.7. Backward from all experts
-// 512 x 64: 1.7 and 3.5, 4096 x 64 2.4 and 3.6 (2.9 at 8192 with eight lanes).
+// 512 x 64: 1.8 and with eight lanes 2.5, 4096 x 64 2.5 and 2.7, 8192 x 64 3.7 and 3.0.
 constexpr int64_t FEW = 4096;
 
 template <typename L, bool BIAS>
@@ -816,8 +820,8 @@ gg_status launch_backward(const Params& p, bool sigmoid, bool renorm, cudaStream
     return p.k <= 8 ? go(Int<8>()) : go(Int<16>());
   }
   const bool wide = p.E % 8 == 0 && !misaligned(p.logits, 16) && !misaligned(p.dlogits, 16);
-  // eight experts a lane: 32768 x 64 bf16 6.0 us, 16411 x 256 fp32 6.9, with sixteen 6.5 and 8.8;
-  // twelve are no whole vectors of bf16 (32768 x 160: 15.3 us, 9.6 with 24)
+  // eight experts a lane: 32768 x 64 bf16 6.2 us, 16411 x 256 fp32 7.3, with sixteen 6.5 and 8.9;
+  // twelve are no whole vectors of bf16 (32768 x 160: 15.9 us, 9.7 with 24)
   by_experts<8, 24, 4>(p.E, p.T <= FEW, [&](auto g, auto nv) {
     constexpr int G = decltype(g)::value, NV = decltype(nv)::value, PER = THREADS / G;
     s = launch("gg_gate_topk_backward", gate_backward_kernel<L, G, NV>,
