@@ -45,8 +45,9 @@ struct Params {
 };
 
 // sigma(x) = 1 / (1 + 2^(-x log2 e)) of a pair, by the hardware's powers and reciprocals. In units
-// of 2^-23 the power is off by 2 + 0.62 |x| (its own error; its argument's two roundings), the sum by
-// 0.5, the reciprocal by 1: 3.5 + 0.62 |x| at most, against half a step of 2^-8 in the bf16 results.
+// of 2^-23 the power is off by 2 + 0.62 |x| (its own error; its argument's two roundings), the sum
+// by 0.5, the reciprocal by 1: 3.5 + 0.62 |x| at most, against half a step of 2^-8 in the bf16
+// results.
 // Below 2^-126 (x < -87.3) it is 0: such gates are done over (FAR).
 __device__ __forceinline__ float2 sigmoid(const float2& x) {
   float2 t = __fmul2_rn(x, both(-1.44269504f));
@@ -76,7 +77,7 @@ __device__ __forceinline__ Gradient gradient(const float2& g, const float2& u, c
 
 // Gates under -87: fp32 holds their sigma (then e^g to the last bit) badly or not at all, while
 // bf16 holds g sigma(g) u down to 2^-133. Their products are made with the fourth root of e^g, one
-// factor after the other. A vector that may have one is told by its bits, or by its block's code.
+// factor after the other. A vector that has one is told by its bits, one that may by its code.
 constexpr float FAR = -87.f;
 constexpr uint32_t FAR_BITS = 0xc2af0000u;  // -87.5, the next bf16, in the upper half of a word
 constexpr uint32_t FAR_CODE = 125;          // the least with which a block can hold 87: 448 / 4
@@ -161,7 +162,8 @@ __device__ __forceinline__ int64_t up_code(const Params& p, int c) {
 // A thread's vectors with far gates, done over when the rest is done. (Beside the rest, as in the
 // backward pass, it takes registers that the 8 bits need: 65536 x 4096 231 us, 169 like this. The
 // backward pass may have written dH or act over its inputs by then; beside the rest it takes 46.8
-// and 50.0 us for 32768 x 1536 from 8 bits and from bf16, 45.6 and 48.6 without it.)
+// and 50.0 us for 32768 x 1536 from 8 bits and from bf16, 45.6 and 48.6 without it. With far gates
+// in every vector it is 53 and 56, forward with the 8 bits 63 instead of 35.)
 __device__ __noinline__ void silu_mul_far(const uint4* H, uint4* act, int32_t concat, int vecs,
                                           int c, int step, float scale) {
   for (; c < vecs; c += step) {
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
     for (int i = 0; i < U; ++i) {
       const int c = c0 + G * i;
       if (c - (int)(threadIdx.x % G) >= vecs) break;  // the row's lanes together
+      far |= any_far(gv[i]);
       float2 g[4], u[4];
       unpack_bf16(gv[i], g);
       unpack_bf16(uv[i], u);
@@ -224,7 +227,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
         uint32_t cg, cu;
         bool odd;
         block_codes(row_mask<G>(), gv[i], uv[i], cg, cu, &odd);
-        far |= cg >= FAR_CODE;
         if (c < vecs) {
           p.H8_out[base + gate_vec(p, c)] = to_e4m3(g, cg, odd);
           p.H8_out[base + up_vec(p, c)] = to_e4m3(u, cu, odd);
@@ -235,7 +237,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) silu_mul_kernel(Params p) {
         }
       }
       if (c < vecs) {
-        if constexpr (!CKPT) far |= any_far(gv[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(silu_times(g[j], u[j]), both(scale));
         p.act[row * vecs + c] = pack_bf16(g);

@@ -65,7 +65,9 @@ def _check_silu_mul(g, u, d, w, concat, ckpt, units):
     _near(dw.cpu().double().numpy(), rdw, size * (units + half) * U + F32_TINY, "dweights")
 
 
-@pytest.mark.parametrize("rows,N,concat", [(33, 256, False), (33, 80, True), (1300, 1040, True)])
+# four and eight lanes a row, a block a row, a warp a row of several pieces
+@pytest.mark.parametrize("rows,N,concat", [(33, 256, False), (33, 80, True), (33, 4096, False),
+                                           (11, 1040, True), (3, 16400, True), (1300, 1040, True)])
 @pytest.mark.parametrize("ckpt", [False, True])
 def test_silu_mul_of_large_gates(rows, N, concat, ckpt):
     """Above 2^8 sigma is 1 or 0, the slope of SiLU too: dg = w d u for every positive gate. A row
@@ -78,7 +80,9 @@ def test_silu_mul_of_large_gates(rows, N, concat, ckpt):
     _check_silu_mul(g, u, d, rng.normal(size=rows), concat, ckpt, 8)
 
 
-@pytest.mark.parametrize("rows,N,concat", [(33, 256, False), (33, 80, True), (1300, 1040, True)])
+# four and eight lanes a row, a block a row, a warp a row of several pieces
+@pytest.mark.parametrize("rows,N,concat", [(33, 256, False), (33, 80, True), (33, 4096, False),
+                                           (11, 1040, True), (3, 16400, True), (1300, 1040, True)])
 @pytest.mark.parametrize("ckpt", [False, True])
 def test_silu_mul_of_far_negative_gates(rows, N, concat, ckpt):
     """Gates whose sigma is below fp32's normal numbers (-87.3) and then below fp32 itself: bf16
@@ -100,8 +104,8 @@ def test_silu_mul_of_far_negative_gates(rows, N, concat, ckpt):
 def test_gate_gradient_of_a_confident_expert(T, E, k, dtype):
     """Softmax over all experts with one of them 8 to 20 above the rest: its gradient
     p (g - sum p_i g_i) = p sum p_i (g - g_i) is many times smaller than g. In units of U: a power
-    is off by 4 and 1.3 times its argument (25 at most), the total and the mean by one of these each, by E / 8
-    additions in a lane and 5 + 5 over the lanes, and there are a few products."""
+    is off by 4 and 1.3 times its argument (25 at most), the total and the mean by one of these each,
+    by E / 8 additions in a lane and 5 + 5 over the lanes, and there are a few products."""
     gen = torch.Generator().manual_seed(E + k)
     x = torch.randn(T, E, generator=gen).clamp(-2.5, 2.5)
     top = torch.randint(0, E, (T, 1), generator=gen)

@@ -16,7 +16,7 @@ def lib():
 
 @pytest.mark.parametrize("f32", [False, True])
 def test_gate_backward_in_place_is_refused(lib, f32):
-    """4 x 8 logits: the gradient in their place, or with the last or first byte among theirs. Apart,
+    """4 x 8 logits: the gradient in their place, or with its first or last number among them. Apart,
     the arguments are in order, and the call gets as far as looking for a device."""
     T, E, size = 4, 8, 4 if f32 else 2
     at = 1 << 20
