@@ -531,7 +531,8 @@ def grouped_mm(A: torch.Tensor, W: torch.Tensor, offs: torch.Tensor,
     (A or W requiring grad) the backward runs gg_dgrad / gg_wgrad and rows past the last
     offset are zero in the output and in dA. Without autograd, ``out`` may be given (rows
     past the last offset are then left as they are). With ``ckpt8`` A is kept for the wgrad in
-    8 bits (``pack8``), about half its bytes, and dW is the product with these values."""
+    8 bits (``pack8``), about half its bytes, and dW is the product with these values. The
+    gradients cannot be differentiated again, and tensors with a tangent are refused."""
     if _wants_grad(A, W):
         if out is not None:
             raise ValueError("out= cannot be used with autograd")
